@@ -9,11 +9,14 @@
 #include <cstring>
 
 #include "../../include/moe.h"
+#include "api_util.h"
 #include "launch.h"
 
 namespace {
-
 thread_local char g_last_error[512] = "";
+}  // namespace
+
+namespace moe_api {
 
 moe_status fail(moe_status status, const char* fmt, ...) {
   va_list ap;
@@ -23,11 +26,10 @@ moe_status fail(moe_status status, const char* fmt, ...) {
   return status;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
+namespace {
 // 0 = unknown, 1 = gfx950, 2 = other arch
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_arch_ok[kMaxDevices];
+}  // namespace
 
 moe_status check_device() {
   int dev = -1;
@@ -55,6 +57,16 @@ moe_status launched(hipError_t err, const char* what) {
   if (err != hipSuccess) return fail(MOE_EDEVICE, "%s: %s", what, hipGetErrorString(err));
   return MOE_OK;
 }
+
+}  // namespace moe_api
+
+using moe_api::aligned16;
+using moe_api::check_device;
+using moe_api::fail;
+using moe_api::kMaxDevices;
+using moe_api::launched;
+
+namespace {
 
 moe_status check_route_dims(int32_t T, int32_t E, int32_t k) {
   if (T < 0) return fail(MOE_EINVAL, "T = %d < 0", T);
@@ -108,12 +120,6 @@ moe_status scratch_of_current_device(void** out) {
   *out = p;
   return MOE_OK;
 }
-
-#define REQUIRE_PTR(p)                                              \
-  do {                                                              \
-    if (!(p)) return fail(MOE_EINVAL, "%s is NULL", #p);            \
-    if (!aligned16(p)) return fail(MOE_EALIGN, "%s is not 16-byte aligned", #p); \
-  } while (0)
 
 }  // namespace
 

@@ -1,0 +1,455 @@
+// libmoe C ABI, block operators (moe_block.h): argument validation, workspace
+// layout, dispatch. As in api.cpp every check runs on the host before anything
+// is enqueued, and nothing here allocates or synchronizes.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "../../include/moe_block.h"
+#include "api_util.h"
+#include "launch_block.h"
+#include "mm.h"
+
+namespace {
+
+using moe_api::check_device;
+using moe_api::fail;
+using moe_api::launched;
+
+constexpr int64_t kMaxFeatures = 1 << 20;    // K and N: 32-bit offsets inside a tile's rows
+constexpr int64_t kMaxResource = 1LL << 30;  // values behind one buffer resource (2 GiB)
+constexpr int64_t kMaxValues = 1LL << 38;    // values of one array: bounds every grid
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+int out_width(const moe_mm_shape* s) { return s->act == MOE_ACT_SWIGLU ? s->N / 2 : s->N; }
+
+moe_status check_mm(const moe_mm_shape* s, bool grouped) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  if (s->rows < 0) return fail(MOE_EINVAL, "rows = %d < 0", s->rows);
+  if (s->dtype != MOE_BF16 && s->dtype != MOE_FP16)
+    return fail(MOE_EINVAL, "dtype = %d is neither MOE_BF16 nor MOE_FP16", s->dtype);
+  if (s->act < MOE_ACT_NONE || s->act > MOE_ACT_SWIGLU)
+    return fail(MOE_EINVAL, "act = %d is not a MOE_ACT_* value", s->act);
+  const int nmod = s->act == MOE_ACT_SWIGLU ? 16 : 8;
+  if (s->K < 8 || s->K % 8 || s->K > kMaxFeatures)
+    return fail(MOE_ESHAPE, "K = %d must be a positive multiple of 8, at most %d", s->K,
+                static_cast<int>(kMaxFeatures));
+  if (s->N < nmod || s->N % nmod || s->N > kMaxFeatures)
+    return fail(MOE_ESHAPE, "N = %d must be a positive multiple of %d, at most %d", s->N, nmod,
+                static_cast<int>(kMaxFeatures));
+  if (static_cast<int64_t>(s->N) * s->K > kMaxResource)
+    return fail(MOE_ESHAPE, "N*K = %lld above 2^30", static_cast<long long>(s->N) * s->K);
+  if (grouped && (s->E < 1 || s->E > MOE_MAX_EXPERTS))
+    return fail(MOE_ESHAPE, "E = %d outside [1, %d]", s->E, MOE_MAX_EXPERTS);
+  const int64_t wide = s->N > s->K ? s->N : s->K;
+  if (s->rows * wide > kMaxValues)
+    return fail(MOE_ESHAPE, "rows*max(N, K) = %lld above 2^38", static_cast<long long>(s->rows * wide));
+  return MOE_OK;
+}
+
+moe_status check_out_type(int32_t type, int32_t dtype, const char* name) {
+  if (type != dtype && type != MOE_F32)
+    return fail(MOE_EINVAL, "%s = %d is neither dtype (%d) nor MOE_F32", name, type, dtype);
+  return MOE_OK;
+}
+
+moe_status check_gather(const moe_mm_shape* s, const int32_t* sorted_slot) {
+  if (!sorted_slot) return MOE_OK;
+  REQUIRE_PTR(sorted_slot);
+  if (s->topk < 1) return fail(MOE_ESHAPE, "topk = %d < 1", s->topk);
+  if (s->x_rows < 1) return fail(MOE_EINVAL, "x_rows = %d < 1", s->x_rows);
+  if (static_cast<int64_t>(s->x_rows) * s->K > kMaxResource)
+    return fail(MOE_ESHAPE, "x_rows*K = %lld above 2^30",
+                static_cast<long long>(s->x_rows) * s->K);
+  return MOE_OK;
+}
+
+moe::MMArgs mm_args(const moe_mm_shape* s, const int32_t* offsets, const int32_t* slot) {
+  moe::MMArgs a = {};
+  a.offsets = offsets;
+  a.slot = slot;
+  a.rows = s->rows;
+  a.x_rows = s->x_rows;
+  a.topk = s->topk;
+  a.E = offsets ? s->E : 1;
+  a.splits = 1;
+  return a;
+}
+
+// Workspace of the gradients: dz, the bias sums' strips, the split products.
+struct MMWs {
+  size_t dz, strips, parts, total;
+};
+MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
+  MMWs w = {};
+  size_t at = 0;
+  w.dz = at;
+  if (!grouped || s->act != MOE_ACT_NONE)
+    at += align256(static_cast<size_t>(s->rows) * s->N * 2);
+  w.strips = at;
+  if (!grouped) at += align256(static_cast<size_t>(moe::dz_strips(s->rows)) * s->N * 4);
+  w.parts = at;
+  const int E = grouped ? s->E : 1, splits = moe::mm_tn_splits(s->rows, E, s->N, s->K);
+  if (splits > 1) at += align256(static_cast<size_t>(E) * splits * s->N * s->K * 4);
+  w.total = at;
+  return w;
+}
+
+// dx = dz W, dw = dz^T x on the given dz
+moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* x, const void* w,
+                             const int32_t* offsets, const int32_t* slot, void* dx, int dx_dtype,
+                             void* dw, int dw_dtype, void* parts, hipStream_t st) {
+  const bool fp16 = s->dtype == MOE_FP16;
+  if (dx && s->rows > 0) {
+    moe::MMArgs a = mm_args(s, offsets, nullptr);
+    a.A = dz;
+    a.B = w;
+    a.C = dx;
+    a.ndim = s->K;
+    a.kdim = s->N;
+    a.c_f32 = dx_dtype == MOE_F32;
+    const moe_status r = launched(moe::launch_mm_nn(a, fp16, st), "row gradient launch");
+    if (r) return r;
+  }
+  if (dw) {
+    moe::MMArgs a = mm_args(s, offsets, slot);
+    a.A = dz;
+    a.B = x;
+    a.mdim = s->N;
+    a.ndim = s->K;
+    a.splits = moe::mm_tn_splits(s->rows, a.E, s->N, s->K);
+    a.C = a.splits > 1 ? parts : dw;
+    a.c_f32 = a.splits > 1 || dw_dtype == MOE_F32;
+    moe_status r = launched(moe::launch_mm_tn(a, fp16, st), "weight gradient launch");
+    if (r) return r;
+    if (a.splits > 1) {
+      r = launched(moe::launch_sum_splits(static_cast<const float*>(parts), a.E, a.splits,
+                                          static_cast<long long>(s->N) * s->K, dw, dw_dtype, st),
+                   "weight gradient sum launch");
+      if (r) return r;
+    }
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* w,
+                          const int32_t* expert_offsets, const int32_t* sorted_slot, void* z,
+                          void* y, int32_t y_dtype, void* stream) {
+  moe_status st = check_mm(shape, true);
+  if (st) return st;
+  if ((st = check_out_type(y_dtype, shape->dtype, "y_dtype"))) return st;
+  if (shape->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(expert_offsets);
+  REQUIRE_PTR(y);
+  if (z) REQUIRE_PTR(z);
+  if ((st = check_gather(shape, sorted_slot))) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::MMArgs a = mm_args(shape, expert_offsets, sorted_slot);
+  a.A = x;
+  a.B = w;
+  a.z = z;
+  a.C = y;
+  a.ndim = shape->N;
+  a.kdim = shape->K;
+  a.act = shape->act;
+  a.c_f32 = y_dtype == MOE_F32;
+  return launched(moe::launch_mm_nt(a, shape->dtype == MOE_FP16, static_cast<hipStream_t>(stream)),
+                  "moe_grouped_mm launch");
+}
+
+size_t moe_grouped_mm_backward_workspace(const moe_mm_shape* shape) {
+  if (check_mm(shape, true)) return 0;
+  return mm_workspace(shape, true).total;
+}
+
+moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy, const void* x,
+                                   const void* w, const void* z, const int32_t* expert_offsets,
+                                   const int32_t* sorted_slot, void* dx, int32_t dx_dtype,
+                                   void* dw, int32_t dw_dtype, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  moe_status st = check_mm(shape, true);
+  if (st) return st;
+  if (!dx && !dw) return fail(MOE_EINVAL, "dx and dw are both NULL");
+  if (dx && (st = check_out_type(dx_dtype, shape->dtype, "dx_dtype"))) return st;
+  if (dw && (st = check_out_type(dw_dtype, shape->dtype, "dw_dtype"))) return st;
+  if (shape->rows == 0 && !dw) return MOE_OK;
+  REQUIRE_PTR(expert_offsets);
+  if (dx) REQUIRE_PTR(dx);
+  if (dw) REQUIRE_PTR(dw);
+  if (shape->rows > 0) {
+    REQUIRE_PTR(dy);
+    if (shape->act != MOE_ACT_NONE) REQUIRE_PTR(z);
+    if (dx) REQUIRE_PTR(w);
+    if (dw) {
+      REQUIRE_PTR(x);
+      if ((st = check_gather(shape, sorted_slot))) return st;
+    }
+  }
+  const MMWs need = mm_workspace(shape, true);
+  if (need.total > 0) {
+    if (ws_bytes < need.total)
+      return fail(MOE_EWORKSPACE, "grouped backward workspace %zu < %zu bytes", ws_bytes, need.total);
+    REQUIRE_PTR(ws);
+  }
+  if ((st = check_device()) != MOE_OK) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const void* dz = dy;
+  if (shape->act != MOE_ACT_NONE) {
+    void* out = base + need.dz;
+    st = launched(moe::launch_dz(dy, false, z, expert_offsets, shape->E, shape->rows, shape->N,
+                                 shape->act, shape->dtype == MOE_FP16, out, nullptr, s),
+                  "activation gradient launch");
+    if (st) return st;
+    dz = out;
+  }
+  return products_backward(shape, dz, x, w, expert_offsets, shape->rows > 0 ? sorted_slot : nullptr,
+                           dx, dx_dtype, dw, dw_dtype, base + need.parts, s);
+}
+
+moe_status moe_linear(const moe_mm_shape* shape, const void* x, const void* w, const void* bias,
+                      const void* residual, void* z, void* y, int32_t y_dtype, void* stream) {
+  moe_status st = check_mm(shape, false);
+  if (st) return st;
+  if ((st = check_out_type(y_dtype, shape->dtype, "y_dtype"))) return st;
+  if (shape->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(y);
+  if (bias) REQUIRE_PTR(bias);
+  if (residual) REQUIRE_PTR(residual);
+  if (z) REQUIRE_PTR(z);
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::MMArgs a = mm_args(shape, nullptr, nullptr);
+  a.A = x;
+  a.B = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.z = z;
+  a.C = y;
+  a.ndim = shape->N;
+  a.kdim = shape->K;
+  a.act = shape->act;
+  a.c_f32 = y_dtype == MOE_F32;
+  return launched(moe::launch_mm_nt(a, shape->dtype == MOE_FP16, static_cast<hipStream_t>(stream)),
+                  "moe_linear launch");
+}
+
+size_t moe_linear_backward_workspace(const moe_mm_shape* shape) {
+  if (check_mm(shape, false)) return 0;
+  return mm_workspace(shape, false).total;
+}
+
+moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_t dy_dtype,
+                               const void* x, const void* w, const void* z, void* dx,
+                               int32_t dx_dtype, void* dw, void* dbias, int32_t dw_dtype, void* ws,
+                               size_t ws_bytes, void* stream) {
+  moe_status st = check_mm(shape, false);
+  if (st) return st;
+  if (!dx && !dw && !dbias) return fail(MOE_EINVAL, "dx, dw and dbias are all NULL");
+  if ((st = check_out_type(dy_dtype, shape->dtype, "dy_dtype"))) return st;
+  if (dx && (st = check_out_type(dx_dtype, shape->dtype, "dx_dtype"))) return st;
+  if ((dw || dbias) && (st = check_out_type(dw_dtype, shape->dtype, "dw_dtype"))) return st;
+  if (shape->rows == 0 && !dw && !dbias) return MOE_OK;
+  if (dx) REQUIRE_PTR(dx);
+  if (dw) REQUIRE_PTR(dw);
+  if (dbias) REQUIRE_PTR(dbias);
+  if (shape->rows > 0) {
+    REQUIRE_PTR(dy);
+    if (shape->act != MOE_ACT_NONE) REQUIRE_PTR(z);
+    if (dx) REQUIRE_PTR(w);
+    if (dw) REQUIRE_PTR(x);
+  }
+  const MMWs need = mm_workspace(shape, false);
+  if (need.total > 0) {
+    if (ws_bytes < need.total)
+      return fail(MOE_EWORKSPACE, "linear backward workspace %zu < %zu bytes", ws_bytes, need.total);
+    REQUIRE_PTR(ws);
+  }
+  if ((st = check_device()) != MOE_OK) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  // dy itself is dz where no activation and no rounding stands between them
+  const bool pass = shape->act != MOE_ACT_NONE || dy_dtype == MOE_F32;
+  const bool want_dz = pass && (dx || dw);
+  float* strips = dbias ? reinterpret_cast<float*>(base + need.strips) : nullptr;
+  const void* dz = want_dz ? base + need.dz : dy;
+  if (want_dz || dbias) {
+    st = launched(moe::launch_dz(dy, dy_dtype == MOE_F32, z, nullptr, 1, shape->rows, shape->N,
+                                 shape->act, shape->dtype == MOE_FP16,
+                                 want_dz ? base + need.dz : nullptr, strips, s),
+                  "activation gradient launch");
+    if (st) return st;
+  }
+  if (dbias) {
+    st = launched(moe::launch_sum_parts(strips, moe::dz_strips(shape->rows), shape->N, dbias,
+                                        dw_dtype, s),
+                  "bias gradient launch");
+    if (st) return st;
+  }
+  if (!dx && !dw) return MOE_OK;
+  return products_backward(shape, dz, x, w, nullptr, nullptr, dx, dx_dtype, dw, dw_dtype,
+                           base + need.parts, s);
+}
+
+static moe_status check_norm(const moe_norm_shape* s) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  if (s->T < 0) return fail(MOE_EINVAL, "T = %d < 0", s->T);
+  if (s->H < 8 || s->H % 8 || s->H > MOE_NORM_MAX_H)
+    return fail(MOE_ESHAPE, "H = %d must be a positive multiple of 8, at most %d", s->H, MOE_NORM_MAX_H);
+  if (s->dtype != MOE_BF16 && s->dtype != MOE_FP16)
+    return fail(MOE_EINVAL, "dtype = %d is neither MOE_BF16 nor MOE_FP16", s->dtype);
+  moe_status st;
+  if ((st = check_out_type(s->r_dtype, s->dtype, "r_dtype"))) return st;
+  if ((st = check_out_type(s->y_dtype, s->dtype, "y_dtype"))) return st;
+  if (s->gate < MOE_GATE_NONE || s->gate > MOE_GATE_ELEMENT)
+    return fail(MOE_EINVAL, "gate = %d is not a MOE_GATE_* value", s->gate);
+  if (!(s->eps > 0.0f) || !std::isfinite(s->eps)) return fail(MOE_EINVAL, "eps must be positive");
+  if (!std::isfinite(s->scale)) return fail(MOE_EINVAL, "scale must be finite");
+  return MOE_OK;
+}
+
+static moe::NormArgs norm_args(const moe_norm_shape* s) {
+  moe::NormArgs a = {};
+  a.T = s->T;
+  a.H = s->H;
+  a.gate_kind = s->gate;
+  a.r_f32 = s->r_dtype == MOE_F32;
+  a.y_f32 = s->y_dtype == MOE_F32;
+  a.scale = s->scale;
+  a.eps = s->eps;
+  return a;
+}
+
+moe_status moe_block_norm(const moe_norm_shape* shape, const void* r, const void* y,
+                          const void* w_post, const void* gate, const void* w_pre, void* r_out,
+                          void* h, void* stream) {
+  moe_status st = check_norm(shape);
+  if (st) return st;
+  if (!r_out && !h) return fail(MOE_EINVAL, "r_out and h are both NULL");
+  if (!h != !w_pre) return fail(MOE_EINVAL, "h and w_pre go together");
+  if (!y && (w_post || r_out || shape->gate != MOE_GATE_NONE))
+    return fail(MOE_EINVAL, "w_post, gate and r_out need y");
+  if (shape->T == 0) return MOE_OK;
+  REQUIRE_PTR(r);
+  if (y) REQUIRE_PTR(y);
+  if (w_post) REQUIRE_PTR(w_post);
+  if (shape->gate != MOE_GATE_NONE) REQUIRE_PTR(gate);
+  if (w_pre) REQUIRE_PTR(w_pre);
+  if (r_out) REQUIRE_PTR(r_out);
+  if (h) REQUIRE_PTR(h);
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::NormArgs a = norm_args(shape);
+  a.r = r;
+  a.y = y;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.r_out = r_out;
+  a.h = h;
+  return launched(moe::launch_block_norm(a, shape->dtype == MOE_FP16, static_cast<hipStream_t>(stream)),
+                  "moe_block_norm launch");
+}
+
+size_t moe_block_norm_backward_workspace(int32_t T, int32_t H) {
+  if (T < 0 || H < 8 || H % 8 || H > MOE_NORM_MAX_H) return 0;
+  return align256(static_cast<size_t>(moe::norm_backward_blocks(T, H)) * 3 * H * 4);
+}
+
+moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* r_out,
+                                   const void* dr_out, const void* dh, const void* y,
+                                   const void* w_post, const void* gate, const void* w_pre,
+                                   void* dr, void* dy, float* dw_post, float* dw_pre, void* dgate,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_norm(shape);
+  if (st) return st;
+  const int T = shape->T, gk = shape->gate;
+  if (!dr_out && !dh) return fail(MOE_EINVAL, "dr_out and dh are both NULL");
+  if (!dh != !w_pre) return fail(MOE_EINVAL, "dh and w_pre go together");
+  if (!y && (w_post || dy || dw_post || dgate || gk != MOE_GATE_NONE))
+    return fail(MOE_EINVAL, "w_post, gate and their gradients need y");
+  if (dw_post && !w_post) return fail(MOE_EINVAL, "dw_post needs w_post");
+  if (dw_pre && !dh) return fail(MOE_EINVAL, "dw_pre needs dh");
+  if (dgate && gk == MOE_GATE_NONE) return fail(MOE_EINVAL, "dgate needs a gate");
+  float* dg_channel = gk == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
+  const bool sums = dw_post || dw_pre || dg_channel;
+  if (T == 0 && !sums) return MOE_OK;
+  if (dw_post) REQUIRE_PTR(dw_post);
+  if (dw_pre) REQUIRE_PTR(dw_pre);
+  if (dgate) REQUIRE_PTR(dgate);
+  if (T > 0) {
+    if (dr_out) REQUIRE_PTR(dr_out);
+    if (dh) {
+      REQUIRE_PTR(dh);
+      REQUIRE_PTR(r_out);
+      REQUIRE_PTR(w_pre);
+    }
+    if (y) REQUIRE_PTR(y);
+    if (w_post) REQUIRE_PTR(w_post);
+    if (gk != MOE_GATE_NONE) REQUIRE_PTR(gate);
+    REQUIRE_PTR(dr);
+    if (dy) REQUIRE_PTR(dy);
+  }
+  const size_t need = moe_block_norm_backward_workspace(T, shape->H);
+  if (sums && need > 0) {
+    if (ws_bytes < need)
+      return fail(MOE_EWORKSPACE, "block norm backward workspace %zu < %zu bytes", ws_bytes, need);
+    REQUIRE_PTR(ws);
+  }
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::NormArgs a = norm_args(shape);
+  a.r = r_out;
+  a.dr_out = dr_out;
+  a.dh = dh;
+  a.y = y;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.dr = dr;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.part = sums ? static_cast<float*>(ws) : nullptr;
+  return launched(moe::launch_block_norm_backward(a, shape->dtype == MOE_FP16, dw_pre, dw_post,
+                                                  dg_channel, static_cast<hipStream_t>(stream)),
+                  "moe_block_norm_backward launch");
+}
+
+moe_status moe_combine_backward(const float* dout, const float* y, const int32_t* slot_pos,
+                                const int32_t* topk_ids, const float* topk_w, int32_t T, int32_t H,
+                                int32_t E, int32_t k, void* dy, int32_t dy_dtype, float* dtopk_w,
+                                float* dlogits, void* stream) {
+  if (T < 0) return fail(MOE_EINVAL, "T = %d < 0", T);
+  if (E < 1 || E > MOE_MAX_EXPERTS) return fail(MOE_ESHAPE, "E = %d outside [1, %d]", E, MOE_MAX_EXPERTS);
+  if (k < 1 || k > E || k > MOE_MAX_TOPK)
+    return fail(MOE_ESHAPE, "k = %d outside [1, min(E=%d, %d)]", k, E, MOE_MAX_TOPK);
+  if (H < 8 || H % 8) return fail(MOE_ESHAPE, "H = %d must be a positive multiple of 8", H);
+  if (static_cast<int64_t>(T) * k >= (1LL << 31))
+    return fail(MOE_ESHAPE, "T*k = %lld does not fit int32", static_cast<long long>(T) * k);
+  if (!dy && !dtopk_w && !dlogits) return fail(MOE_EINVAL, "dy, dtopk_w and dlogits are all NULL");
+  if (dy && dy_dtype != MOE_BF16 && dy_dtype != MOE_FP16 && dy_dtype != MOE_F32)
+    return fail(MOE_EINVAL, "dy_dtype = %d is no MOE_BF16, MOE_FP16 or MOE_F32", dy_dtype);
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(dout);
+  REQUIRE_PTR(slot_pos);
+  REQUIRE_PTR(topk_w);
+  if (dtopk_w || dlogits) REQUIRE_PTR(y);
+  if (dlogits) REQUIRE_PTR(topk_ids);
+  if (dy) REQUIRE_PTR(dy);
+  if (dtopk_w) REQUIRE_PTR(dtopk_w);
+  if (dlogits) REQUIRE_PTR(dlogits);
+  moe_status st;
+  if ((st = check_device()) != MOE_OK) return st;
+  return launched(moe::launch_combine_backward(dout, y, slot_pos, topk_ids, topk_w, T, H, E, k, dy,
+                                               dy ? dy_dtype : MOE_F32, dtopk_w, dlogits,
+                                               static_cast<hipStream_t>(stream)),
+                  "moe_combine_backward launch");
+}
+
+}  // extern "C"

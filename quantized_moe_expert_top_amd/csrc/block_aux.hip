@@ -1,0 +1,210 @@
+// Passes beside the gradient products: dz = act'(z) dy with the bias gradient's
+// partial sums, and sums of float32 parts.
+#include "launch_block.h"
+#include "mm.h"
+
+namespace moe {
+namespace {
+
+template <class T>
+__device__ __forceinline__ void load8(const void* p, size_t at, bool f32, float (&v)[8]) {
+  if (f32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 w = ld16(static_cast<const uint16_t*>(p) + at);
+    unpack2<T>(w.x, v[0], v[1]);
+    unpack2<T>(w.y, v[2], v[3]);
+    unpack2<T>(w.z, v[4], v[5]);
+    unpack2<T>(w.w, v[6], v[7]);
+  }
+}
+template <class T>
+__device__ __forceinline__ void store8(void* p, size_t at, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+      make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                 pack2<T>(v[6], v[7]));
+}
+
+// A block takes 512 columns of dy (8 per thread) and a strip of rows, four at a
+// time; bound by the bytes of dy, z and dz. The column sums stay in registers
+// over the strip and are joined in LDS in a fixed order.
+constexpr int kDzCols = 512;
+
+template <class T, bool SWIGLU>
+__global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, int dy_f32,
+                                                 const void* __restrict__ z,
+                                                 const int* __restrict__ offsets, int E, int rows,
+                                                 int N, int act, int strip_rows, int col_blocks,
+                                                 void* __restrict__ dz, float* __restrict__ part) {
+  constexpr int S = SWIGLU ? 2 : 1;
+  __shared__ float red[3][S][kDzCols];
+  const int No = SWIGLU ? N / 2 : N;
+  const int cb = blockIdx.x % col_blocks, strip = blockIdx.x / col_blocks;
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const int col = cb * kDzCols + tx * 8;
+  int lo = 0, hi = rows;
+  if (offsets) {
+    lo = min(max(offsets[0], 0), rows);
+    hi = min(max(offsets[E], lo), rows);
+  }
+  // 64-bit: the last strip's end may pass 2^31
+  const long long r0 = static_cast<long long>(strip) * strip_rows;
+  const long long r1 = min(r0 + strip_rows, static_cast<long long>(hi));
+  float sum[S][8];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[s][i] = 0.0f;
+  if (col < No) {
+#pragma unroll 2
+    for (long long r = max(r0, static_cast<long long>(lo)) + ty; r < r1; r += 4) {
+      float d[8], g[8];
+      load8<T>(dy, r * No + col, dy_f32, d);
+      if (SWIGLU) {
+        float u[8], du[8];
+        load8<T>(z, r * N + col, false, g);
+        load8<T>(z, r * N + No + col, false, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float sg = sigmoid_f32(g[i]);
+          du[i] = d[i] * g[i] * sg;
+          d[i] = d[i] * u[i] * (sg * (1.0f + g[i] * (1.0f - sg)));
+        }
+        if (dz) {
+          store8<T>(dz, r * N + col, d);
+          store8<T>(dz, r * N + No + col, du);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[S - 1][i] += du[i];
+      } else {
+        if (act != 0) {
+          load8<T>(z, r * N + col, false, g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] *= act_grad_f32(g[i], act);
+        }
+        if (dz) store8<T>(dz, r * N + col, d);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0][i] += d[i];
+    }
+  }
+  if (part == nullptr) return;
+  if (ty > 0)
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) red[ty - 1][s][tx * 8 + i] = sum[s][i];
+  __syncthreads();
+  if (ty == 0 && col < No)
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v = sum[s][i];
+#pragma unroll
+        for (int y = 0; y < 3; ++y) v += red[y][s][tx * 8 + i];
+        part[static_cast<size_t>(strip) * N + s * No + col + i] = v;
+      }
+}
+
+__device__ __forceinline__ void store_as(void* out, long long i, float v, int type) {
+  if (type == 2) static_cast<float*>(out)[i] = v;
+  else if (type == 0) static_cast<uint16_t*>(out)[i] = f32_to_bf16(v);
+  else static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack2<fp16_tag>(v, 0.0f));
+}
+
+// 32 columns x 8 runs of parts per block; the runs are joined in order.
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ part, int parts,
+                                                        long long n, void* __restrict__ out,
+                                                        int type) {
+  __shared__ float red[8][32];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const long long col = static_cast<long long>(blockIdx.x) * 32 + tx;
+  const int run = (parts + 7) / 8, p0 = ty * run, p1 = min(p0 + run, parts);
+  float v = 0.0f;
+  if (col < n)
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) v += part[static_cast<size_t>(p) * n + col];
+  red[ty][tx] = v;
+  __syncthreads();
+  if (ty == 0 && col < n) {
+    for (int y = 1; y < 8; ++y) v += red[y][tx];
+    store_as(out, col, v, type);
+  }
+}
+
+__global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part,
+                                                         int splits, long long n4, long long total4,
+                                                         void* __restrict__ out, int type) {
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total4;
+       i += static_cast<long long>(gridDim.x) * 256) {
+    const long long e = i / n4, c = i - e * n4;
+    const float4* p = reinterpret_cast<const float4*>(part) + e * splits * n4 + c;
+    float4 v = p[0];
+    for (int s = 1; s < splits; ++s) {
+      const float4 w = p[s * n4];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    if (type == 2) {
+      reinterpret_cast<float4*>(out)[i] = v;
+    } else if (type == 0) {
+      reinterpret_cast<uint2*>(out)[i] = make_uint2(pack2<bf16_tag>(v.x, v.y), pack2<bf16_tag>(v.z, v.w));
+    } else {
+      reinterpret_cast<uint2*>(out)[i] = make_uint2(pack2<fp16_tag>(v.x, v.y), pack2<fp16_tag>(v.z, v.w));
+    }
+  }
+}
+
+int strip_rows_of(int rows) {
+  const int r = (rows + 511) / 512;
+  return r < 64 ? 64 : r;
+}
+
+}  // namespace
+
+int dz_strips(int rows) {
+  const int sr = strip_rows_of(rows);
+  return static_cast<int>((static_cast<long long>(rows) + sr - 1) / sr);
+}
+
+hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
+                     int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s) {
+  if (rows == 0) return hipSuccess;
+  const int No = act == kActSwiglu ? N / 2 : N;
+  const int cb = (No + kDzCols - 1) / kDzCols;
+  const int sr = strip_rows_of(rows);
+  const dim3 grid(static_cast<unsigned>(dz_strips(rows)) * cb), block(256);
+  const int f = dy_f32;
+  if (act == kActSwiglu) {
+    if (fp16) dz_kernel<fp16_tag, true><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
+    else dz_kernel<bf16_tag, true><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
+  } else {
+    if (fp16) dz_kernel<fp16_tag, false><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
+    else dz_kernel<bf16_tag, false><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_parts(const float* part, int parts, long long n, void* out, int out_type,
+                            hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>((n + 31) / 32);
+  sum_parts_kernel<<<grid, 256, 0, s>>>(part, parts, n, out, out_type);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_splits(const float* part, int E, int splits, long long n, void* out,
+                             int out_type, hipStream_t s) {
+  const long long n4 = n / 4, total4 = n4 * E;
+  const long long blocks = (total4 + 255) / 256;
+  sum_splits_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(
+      part, splits, n4, total4, out, out_type);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,104 @@
+// Gradients of the weighted combine and of the softmax over a token's picks.
+//
+//   dy[pos(t, j)] = w_tj dout_t        dw_tj = <dout_t, y[pos(t, j)]>
+//   dlogits[t, id_tj] = w_tj (dw_tj - sum_i w_ti dw_ti),  0 elsewhere
+//
+// Bound by the bytes of y and dy. A block takes a token, a wave one pick at a
+// time over the whole row, so a pick's dot product is one wave sum in a fixed
+// order and all k rows are in flight at once; dout comes from the caches after
+// its first read.
+#include "launch_block.h"
+#include "mm.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxPicks = 32;
+
+template <int DY>   // 0 bf16, 1 fp16, 2 float32
+__device__ __forceinline__ void store_dy(void* dy, size_t at, const float4& a, const float4& b) {
+  if constexpr (DY == 2) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(dy) + at);
+    q[0] = a;
+    q[1] = b;
+  } else {
+    using T = typename std::conditional<DY == 0, bf16_tag, fp16_tag>::type;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dy) + at) =
+        make_uint4(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w), pack2<T>(b.x, b.y), pack2<T>(b.z, b.w));
+  }
+}
+
+template <int DY>
+__global__ __launch_bounds__(512) void combine_backward_kernel(
+    const float* __restrict__ dout, const float* __restrict__ y, const int* __restrict__ slot_pos,
+    const int* __restrict__ ids, const float* __restrict__ w, int T, int H, int E, int k,
+    void* __restrict__ dy, float* __restrict__ dw, float* __restrict__ dlogits) {
+  __shared__ float sdw[kMaxPicks];
+  __shared__ float swt[kMaxPicks];
+  __shared__ int sid[kMaxPicks];
+  const int t = blockIdx.x, lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
+  const int waves = blockDim.x >> 6;
+  const int C = H / 8;
+  const long long R = static_cast<long long>(T) * k;
+  const float* drow = dout + static_cast<size_t>(t) * H;
+  const bool need_dot = dw != nullptr || dlogits != nullptr;
+  for (int j = wv; j < k; j += waves) {
+    const size_t f = static_cast<size_t>(t) * k + j;
+    long long p = slot_pos[f];
+    p = p < 0 ? 0 : p >= R ? R - 1 : p;
+    const float wj = w[f];
+    const size_t row = static_cast<size_t>(p) * H;
+    float dot = 0.0f;
+#pragma unroll 4
+    for (int c = lane; c < C; c += kWave) {
+      const float4* d4 = reinterpret_cast<const float4*>(drow + c * 8);
+      const float4 d0 = d4[0], d1 = d4[1];
+      if (need_dot) {
+        const float4* y4 = reinterpret_cast<const float4*>(y + row + c * 8);
+        const float4 y0 = y4[0], y1 = y4[1];
+        dot += d0.x * y0.x + d0.y * y0.y + d0.z * y0.z + d0.w * y0.w + d1.x * y1.x + d1.y * y1.y +
+               d1.z * y1.z + d1.w * y1.w;
+      }
+      if (dy)
+        store_dy<DY>(dy, row + c * 8, make_float4(wj * d0.x, wj * d0.y, wj * d0.z, wj * d0.w),
+                     make_float4(wj * d1.x, wj * d1.y, wj * d1.z, wj * d1.w));
+    }
+    if (need_dot) {
+      dot = wave_sum_f32(dot);
+      if (lane == 0) {
+        if (dw) dw[f] = dot;
+        sdw[j] = dot;
+        swt[j] = wj;
+        if (dlogits) sid[j] = ids[f];
+      }
+    }
+  }
+  if (dlogits == nullptr) return;   // uniform
+  __syncthreads();
+  float mean = 0.0f;
+  for (int j = 0; j < k; ++j) mean += swt[j] * sdw[j];
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float v = 0.0f;
+    for (int j = 0; j < k; ++j) v += sid[j] == e ? swt[j] * (sdw[j] - mean) : 0.0f;
+    dlogits[static_cast<size_t>(t) * E + e] = v;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_combine_backward(const float* dout, const float* y, const int* slot_pos,
+                                   const int* ids, const float* w, int T, int H, int E, int k,
+                                   void* dy, int dy_type, float* dw, float* dlogits,
+                                   hipStream_t s) {
+  if (T == 0) return hipSuccess;
+  const int threads = k > 4 ? 512 : k > 2 ? 256 : k > 1 ? 128 : 64;
+  if (dy_type == 0)
+    combine_backward_kernel<0><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+  else if (dy_type == 1)
+    combine_backward_kernel<1><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+  else
+    combine_backward_kernel<2><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+  return hipGetLastError();
+}
+
+}  // namespace moe

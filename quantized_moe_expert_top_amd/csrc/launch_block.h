@@ -1,0 +1,57 @@
+// Host-side launchers of the block operators (moe_block.h). Arguments have been
+// validated by block_api.cpp; each returns the launch status.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct MMArgs;
+hipError_t launch_mm_nt(const MMArgs& a, bool fp16, hipStream_t s);
+hipError_t launch_mm_nn(const MMArgs& a, bool fp16, hipStream_t s);
+hipError_t launch_mm_tn(const MMArgs& a, bool fp16, hipStream_t s);
+int mm_tn_splits(int rows, int E, int mdim, int ndim);
+
+// dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
+// (part [dz_strips(rows)][N], may be NULL). offsets NULL: all rows; otherwise
+// rows [offsets[0], offsets[E]).
+int dz_strips(int rows);
+hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
+                     int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s);
+// out[n] = sum over parts, in order; out_type 0 bf16, 1 fp16, 2 float32
+hipError_t launch_sum_parts(const float* part, int parts, long long n, void* out, int out_type,
+                            hipStream_t s);
+// the same per expert: out[e][n] = sum_s part[e][s][n] (n a multiple of 4)
+hipError_t launch_sum_splits(const float* part, int E, int splits, long long n, void* out,
+                             int out_type, hipStream_t s);
+
+struct NormArgs {
+  const void* r;        // forward: r; backward: r_out
+  const void* y;
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+  void* r_out;
+  void* h;
+  const void* dr_out;
+  const void* dh;
+  void* dr;
+  void* dy;
+  void* dgate;
+  float* part;          // [blocks][3][H]: dw_pre, dw_post, dgate
+  int T, H, gate_kind;
+  int r_f32, y_f32;
+  float scale, eps;
+};
+hipError_t launch_block_norm(const NormArgs& a, bool fp16, hipStream_t s);
+int norm_backward_blocks(int T, int H);
+hipError_t launch_block_norm_backward(const NormArgs& a, bool fp16, float* dw_pre, float* dw_post,
+                                      float* dgate_channel, hipStream_t s);
+
+hipError_t launch_combine_backward(const float* dout, const float* y, const int* slot_pos,
+                                   const int* ids, const float* w, int T, int H, int E, int k,
+                                   void* dy, int dy_type, float* dw, float* dlogits,
+                                   hipStream_t s);
+
+}  // namespace moe

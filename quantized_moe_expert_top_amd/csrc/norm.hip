@@ -1,0 +1,416 @@
+// Norms before and after a block, fused with the block's gate and residual
+// scale, forward and backward (moe_block_norm, moe_block_norm_backward).
+//
+//   n = y p w_post, p = 1/sqrt(mean(y^2) + eps);   r' = r + c g n
+//   h = r' q w_pre, q = 1/sqrt(mean(r'^2) + eps)
+//
+// backward, with d = dh w_pre (per element) and sums over a row's H elements:
+//   dr  = dr' + q d - r' q^3 sum(d r') / H          dw_pre  = sum_t dh r' q
+//   dn  = c g dr;  e = dn w_post
+//   dy  = p e - y p^3 sum(e y) / H                  dw_post = sum_t dn y p
+//   dg  = c dr n  (summed over tokens or over the row, as the gate broadcasts)
+//
+// Both are bound by the bytes of the rows: every row is read once and stays in
+// registers over its two reductions.
+#include "launch_block.h"
+#include "mm.h"
+
+namespace moe {
+namespace {
+
+template <class T>
+__device__ __forceinline__ void row_load8(const void* p, size_t at, bool f32, float (&v)[8]) {
+  if (f32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 w = ld16(static_cast<const uint16_t*>(p) + at);
+    unpack2<T>(w.x, v[0], v[1]);
+    unpack2<T>(w.y, v[2], v[3]);
+    unpack2<T>(w.z, v[4], v[5]);
+    unpack2<T>(w.w, v[6], v[7]);
+  }
+}
+template <class T>
+__device__ __forceinline__ void row_store8(void* p, size_t at, bool f32, const float (&v)[8]) {
+  if (f32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+        make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                   pack2<T>(v[6], v[7]));
+  }
+}
+template <class T>
+__device__ __forceinline__ float load1(const void* p, size_t at) {
+  float lo, hi;
+  unpack2<T>(static_cast<const uint16_t*>(p)[at], lo, hi);
+  return lo;
+}
+
+// Sum over a row held by WPR waves; every thread gets it. `red` holds WPR
+// floats and is free again after the next call's barrier (two slots alternate).
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum_f32(v);
+  if constexpr (WPR == 1) return v;
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x >> 6;
+  if (lane == 0) red[w] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) s += red[i];
+  return s;
+}
+
+// A row is held by WPR waves, NC chunks of 8 per thread; WPR = 1 puts four rows
+// in a block.
+template <class T, int WPR, int NC>
+__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void block_norm_kernel(const NormArgs a) {
+  constexpr int kRows = WPR == 1 ? 4 : 1, kRowThreads = WPR * kWave;
+  __shared__ float red[2][WPR];
+  const int rt = WPR == 1 ? (threadIdx.x & (kWave - 1)) : threadIdx.x;
+  const int t = blockIdx.x * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0);
+  if (t >= a.T) return;   // whole waves; with WPR > 1, whole blocks
+  const int C = a.H / 8;
+  const size_t row = static_cast<size_t>(t) * a.H;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  float r[NC][8];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = rt + i * kRowThreads;
+    if (c < C) row_load8<T>(a.r, row + c * 8, a.r_f32, r[i]);
+    else
+#pragma unroll
+      for (int x = 0; x < 8; ++x) r[i][x] = 0.0f;
+  }
+  if (a.y) {
+    float y[NC][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = rt + i * kRowThreads;
+      if (c < C) row_load8<T>(a.y, row + c * 8, a.y_f32, y[i]);
+      else
+#pragma unroll
+        for (int x = 0; x < 8; ++x) y[i][x] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) ss += y[i][x] * y[i][x];
+    }
+    float f = a.scale;
+    if (a.gate_kind == 2) f *= load1<T>(a.gate, t);
+    if (a.w_post) f *= 1.0f / sqrtf(row_sum<WPR>(ss, red[0]) * inv_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = rt + i * kRowThreads;
+      if (c >= C) continue;
+      if (a.w_post) {
+        float w[8];
+        row_load8<T>(a.w_post, static_cast<size_t>(c) * 8, false, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) y[i][x] *= w[x];
+      }
+      if (a.gate_kind == 1 || a.gate_kind == 3) {
+        float g[8];
+        row_load8<T>(a.gate, (a.gate_kind == 3 ? row : 0) + c * 8, false, g);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) y[i][x] *= g[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) r[i][x] += f * y[i][x];
+      if (a.r_out) row_store8<T>(a.r_out, row + c * 8, a.r_f32, r[i]);
+    }
+  }
+  if (a.h) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) ss += r[i][x] * r[i][x];
+    const float q = 1.0f / sqrtf(row_sum<WPR>(ss, red[1]) * inv_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = rt + i * kRowThreads;
+      if (c >= C) continue;
+      float w[8];
+      row_load8<T>(a.w_pre, static_cast<size_t>(c) * 8, false, w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) r[i][x] *= q * w[x];
+      row_store8<T>(a.h, row + c * 8, false, r[i]);
+    }
+  }
+}
+
+// Sums of three values over a row held by a whole block of W waves. `red` has
+// two halves that alternate between calls, so one barrier per call is enough.
+template <int W>
+__device__ __forceinline__ void block_sum3(float& u, float& v, float& w, float (*red)[3]) {
+  u = wave_sum_f32(u);
+  v = wave_sum_f32(v);
+  w = wave_sum_f32(w);
+  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
+  if (lane == 0) {
+    red[wv][0] = u;
+    red[wv][1] = v;
+    red[wv][2] = w;
+  }
+  __syncthreads();
+  u = v = w = 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    u += red[i][0];
+    v += red[i][1];
+    w += red[i][2];
+  }
+}
+
+// What one thread holds of a row: a chunk of 8 of each operand.
+struct NormChunk {
+  float dr[8], y[8], x[8], d[8];   // dr', y, r', dh
+};
+template <class T>
+__device__ __forceinline__ void norm_chunk_load(const NormArgs& a, size_t at, bool in, NormChunk& v) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) v.dr[x] = v.y[x] = v.x[x] = v.d[x] = 0.0f;
+  if (!in) return;
+  if (a.dr_out) row_load8<T>(a.dr_out, at, a.r_f32, v.dr);
+  if (a.y) row_load8<T>(a.y, at, a.y_f32, v.y);
+  if (a.dh) {
+    row_load8<T>(a.r, at, a.r_f32, v.x);
+    row_load8<T>(a.dh, at, false, v.d);
+  }
+}
+// v.dr becomes the whole gradient of r'
+template <class T>
+__device__ __forceinline__ void norm_chunk_dr(const NormArgs& a, int c, float q, float back,
+                                              NormChunk& v) {
+  if (!a.dh) return;
+  float w[8];
+  row_load8<T>(a.w_pre, static_cast<size_t>(c) * 8, false, w);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) v.dr[x] += q * v.d[x] * w[x] - v.x[x] * back;
+}
+template <class T>
+__device__ __forceinline__ void norm_chunk_post(const NormArgs& a, int c, size_t at, float tg,
+                                                float (&w)[8], float (&g)[8]) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    w[x] = 1.0f;
+    g[x] = tg;
+  }
+  if (a.w_post) row_load8<T>(a.w_post, static_cast<size_t>(c) * 8, false, w);
+  if (a.gate_kind == 1 || a.gate_kind == 3)
+    row_load8<T>(a.gate, a.gate_kind == 3 ? at : static_cast<size_t>(c) * 8, false, g);
+}
+
+// Rows blockIdx, blockIdx + grid, ...; the sums over tokens stay in registers
+// and go to part[blockIdx] at the end, joined in order afterwards. RELOAD: rows
+// too wide to stay in registers beside the sums (H > 8192) are read again, from
+// L2, in each of the three phases, and the sums live in part[blockIdx] all along.
+template <class T, int W, int NC, bool RELOAD>
+__global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(const NormArgs a) {
+  constexpr int kThr = W * kWave, kHeld = RELOAD ? 1 : NC;
+  __shared__ float red[2][W][3];
+  const int C = a.H / 8;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  float* part = a.part ? a.part + static_cast<size_t>(blockIdx.x) * 3 * a.H : nullptr;
+  float sw_pre[kHeld][8], sw_post[kHeld][8], sg[kHeld][8];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sw_pre[i][x] = sw_post[i][x] = sg[i][x] = 0.0f;
+  constexpr int kUnroll = RELOAD ? 1 : NC;
+
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t row = static_cast<size_t>(t) * a.H;
+    NormChunk v[kHeld];
+    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    if constexpr (!RELOAD) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * kThr;
+        norm_chunk_load<T>(a, row + c * 8, c < C, v[i]);
+      }
+    }
+#pragma unroll kUnroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * kThr;
+      NormChunk& u = v[RELOAD ? 0 : i];
+      if constexpr (RELOAD) norm_chunk_load<T>(a, row + c * 8, c < C, u);
+      if (c >= C) continue;
+      if (a.dh) {
+        float w[8];
+        row_load8<T>(a.w_pre, static_cast<size_t>(c) * 8, false, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          s1 += u.x[x] * u.x[x];
+          s2 += u.d[x] * w[x] * u.x[x];
+        }
+      }
+      if (a.y)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s3 += u.y[x] * u.y[x];
+    }
+    block_sum3<W>(s1, s2, s3, red[0]);
+    const float q = 1.0f / sqrtf(s1 * inv_h + a.eps);
+    const float p = a.w_post ? 1.0f / sqrtf(s3 * inv_h + a.eps) : 1.0f;
+    const float back = q * q * q * s2 * inv_h;
+    const float tg = a.gate_kind == 2 ? load1<T>(a.gate, t) : 1.0f;
+    float s4 = 0.0f, s5 = 0.0f, s6 = 0.0f;
+#pragma unroll kUnroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * kThr;
+      NormChunk& u = v[RELOAD ? 0 : i];
+      if constexpr (RELOAD) norm_chunk_load<T>(a, row + c * 8, c < C, u);
+      if (c >= C) continue;
+      norm_chunk_dr<T>(a, c, q, back, u);
+      const int hi = RELOAD ? 0 : i;   // where this chunk's sums are held
+      if (RELOAD && part && t != blockIdx.x) {
+        row_load8<T>(part, static_cast<size_t>(c) * 8, true, sw_pre[0]);
+        row_load8<T>(part, static_cast<size_t>(a.H) + c * 8, true, sw_post[0]);
+        row_load8<T>(part, static_cast<size_t>(a.H) * 2 + c * 8, true, sg[0]);
+      } else if (RELOAD) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sw_pre[0][x] = sw_post[0][x] = sg[0][x] = 0.0f;
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sw_pre[hi][x] += u.d[x] * u.x[x] * q;
+      row_store8<T>(a.dr, row + c * 8, a.r_f32, u.dr);
+      if (a.y) {
+        float w[8], g[8], dg[8];
+        norm_chunk_post<T>(a, c, row + c * 8, tg, w, g);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float cd = a.scale * u.dr[x], dn = cd * g[x], yp = u.y[x] * p;
+          dg[x] = cd * yp * w[x];
+          sw_post[hi][x] += dn * yp;
+          u.d[x] = dn * w[x];            // from here d holds e = dn w_post
+          s4 += u.d[x] * u.y[x];
+          s5 += dg[x];
+          sg[hi][x] += dg[x];
+        }
+        if (a.gate_kind == 3 && a.dgate) row_store8<T>(a.dgate, row + c * 8, false, dg);
+      }
+      if (RELOAD && part) {
+        row_store8<T>(part, static_cast<size_t>(c) * 8, true, sw_pre[0]);
+        row_store8<T>(part, static_cast<size_t>(a.H) + c * 8, true, sw_post[0]);
+        row_store8<T>(part, static_cast<size_t>(a.H) * 2 + c * 8, true, sg[0]);
+      }
+    }
+    if (a.y) {
+      block_sum3<W>(s4, s5, s6, red[1]);
+      const float bk = a.w_post ? p * p * p * s4 * inv_h : 0.0f;
+      if (a.dy)
+#pragma unroll kUnroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = threadIdx.x + i * kThr;
+          NormChunk& u = v[RELOAD ? 0 : i];
+          if (c >= C) continue;
+          if constexpr (RELOAD) {
+            norm_chunk_load<T>(a, row + c * 8, true, u);
+            norm_chunk_dr<T>(a, c, q, back, u);
+            float w[8], g[8];
+            norm_chunk_post<T>(a, c, row + c * 8, tg, w, g);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) u.d[x] = a.scale * u.dr[x] * g[x] * w[x];
+          }
+          float o[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) o[x] = p * u.d[x] - u.y[x] * bk;
+          row_store8<T>(a.dy, row + c * 8, a.y_f32, o);
+        }
+      if (a.gate_kind == 2 && a.dgate && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = s5;
+    } else {
+      __syncthreads();   // the next row writes red[0] again
+    }
+  }
+  if (RELOAD || part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = threadIdx.x + i * kThr;
+    if (c >= C) continue;
+    row_store8<T>(part, static_cast<size_t>(c) * 8, true, sw_pre[i]);
+    row_store8<T>(part, static_cast<size_t>(a.H) + c * 8, true, sw_post[i]);
+    row_store8<T>(part, static_cast<size_t>(a.H) * 2 + c * 8, true, sg[i]);
+  }
+}
+
+// part [blocks][3][H] -> the outputs that are asked for, sums in block order
+// over 8 runs.
+__global__ __launch_bounds__(256) void norm_parts_kernel(const float* __restrict__ part, int parts,
+                                                         int H, float* __restrict__ o0,
+                                                         float* __restrict__ o1,
+                                                         float* __restrict__ o2) {
+  __shared__ float red[8][32];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + tx, which = blockIdx.y;
+  float* out = which == 0 ? o0 : which == 1 ? o1 : o2;
+  if (out == nullptr) return;   // uniform
+  const int run = (parts + 7) / 8, p0 = ty * run, p1 = min(p0 + run, parts);
+  float v = 0.0f;
+  if (col < H)
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) v += part[(static_cast<size_t>(p) * 3 + which) * H + col];
+  red[ty][tx] = v;
+  __syncthreads();
+  if (ty == 0 && col < H) {
+    for (int y = 1; y < 8; ++y) v += red[y][tx];
+    out[col] = v;
+  }
+}
+
+template <class T>
+hipError_t forward(const NormArgs& a, hipStream_t s) {
+  const int C = a.H / 8;
+  const auto four = dim3((a.T + 3) / 4);
+  if (C <= 64) block_norm_kernel<T, 1, 1><<<four, 256, 0, s>>>(a);
+  else if (C <= 256) block_norm_kernel<T, 4, 1><<<a.T, 256, 0, s>>>(a);
+  else if (C <= 512) block_norm_kernel<T, 4, 2><<<a.T, 256, 0, s>>>(a);
+  else if (C <= 1024) block_norm_kernel<T, 16, 1><<<a.T, 1024, 0, s>>>(a);
+  else block_norm_kernel<T, 16, 2><<<a.T, 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t backward(const NormArgs& a, int blocks, hipStream_t s) {
+  const int C = a.H / 8;
+  if (C <= 64) block_norm_backward_kernel<T, 1, 1, false><<<blocks, 64, 0, s>>>(a);
+  else if (C <= 256) block_norm_backward_kernel<T, 4, 1, false><<<blocks, 256, 0, s>>>(a);
+  else if (C <= 512) block_norm_backward_kernel<T, 8, 1, false><<<blocks, 512, 0, s>>>(a);
+  else if (C <= 1024) block_norm_backward_kernel<T, 16, 1, false><<<blocks, 1024, 0, s>>>(a);
+  else block_norm_backward_kernel<T, 16, 2, true><<<blocks, 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const NormArgs& a, bool fp16, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  return fp16 ? forward<fp16_tag>(a, s) : forward<bf16_tag>(a, s);
+}
+
+int norm_backward_blocks(int T, int H) {
+  const int most = H <= 2048 ? 1024 : 512;
+  return T < most ? T : most;
+}
+
+hipError_t launch_block_norm_backward(const NormArgs& a, bool fp16, float* dw_pre, float* dw_post,
+                                      float* dgate_channel, hipStream_t s) {
+  const int blocks = norm_backward_blocks(a.T, a.H);
+  if (a.T > 0) {
+    const hipError_t e = fp16 ? backward<fp16_tag>(a, blocks, s) : backward<bf16_tag>(a, blocks, s);
+    if (e != hipSuccess) return e;
+  }
+  if (dw_pre || dw_post || dgate_channel) {
+    norm_parts_kernel<<<dim3((a.H + 31) / 32, 3), 256, 0, s>>>(a.part, blocks, a.H, dw_pre,
+                                                               dw_post, dgate_channel);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe
