@@ -35,11 +35,14 @@ typedef __attribute__((__vector_size__(2 * sizeof(_Float16)))) _Float16 f16x2_t;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
+typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2_t;
+typedef i32x4_t frag_t;   // 8 values of one operand
+
 struct bf16_tag {};
 struct fp16_tag {};
 
 template <class T>
-__device__ __forceinline__ f32x16_t mfma16(uint4 a, uint4 b, f32x16_t c) {
+__device__ __forceinline__ f32x16_t mfma16(frag_t a, frag_t b, f32x16_t c) {
   if constexpr (__is_same(T, bf16_tag))
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
@@ -96,6 +99,33 @@ __device__ __forceinline__ float act_grad_f32(float z, int act) {
   return 1.0f;
 }
 
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+__device__ __forceinline__ void mm_area8(const float* p, float (&v)[8]) {
+  const f32x4_t a = reinterpret_cast<const f32x4_t*>(p)[0], b = reinterpret_cast<const f32x4_t*>(p)[1];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    v[t] = a[t];
+    v[4 + t] = b[t];
+  }
+}
+template <class T>
+__device__ __forceinline__ void mm_add8(const uint16_t* p, float (&v)[8]) {
+  const uint4 w = ld16(p);
+  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    float lo, hi;
+    unpack2<T>(d[t], lo, hi);
+    v[2 * t] += lo;
+    v[2 * t + 1] += hi;
+  }
+}
+template <class T>
+__device__ __forceinline__ void mm_store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
+                                            pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+}
+
 enum { kModeNT = 0, kModeNN = 1, kModeTN = 2 };
 constexpr int kActSwiglu = 4;
 
@@ -133,12 +163,13 @@ struct MMGeom {
   static constexpr int kASlots = BM * BK / 8, kBSlots = BN * BK / 8;   // 16-byte slots
   static constexpr int kAPer = kASlots / kThreads, kBPer = kBSlots / kThreads;
   static constexpr int kStageBytes = (kASlots + kBSlots) * 16;
-  static constexpr int kLds = STAGES * kStageBytes;
+  static constexpr int kAreaBytes = WM * WN * 32 * (BN / WN + 4) * 4;   // epilogue
+  static constexpr int kLds = STAGES * kStageBytes > kAreaBytes ? STAGES * kStageBytes : kAreaBytes;
   static constexpr int kLoads = kAPer + kBPer;                 // per thread and stage
   static_assert(kASlots % kThreads == 0 && kBSlots % kThreads == 0, "slots split evenly");
   static_assert(kAPer >= 1 && kAPer <= 8 && kBPer >= 1 && kBPer <= 8, "slot arrays hold eight");
   static_assert(MI >= 1 && MI <= 4 && NJ >= 1 && NJ <= 4, "accumulator array holds 4 x 4");
-  static_assert(BK == 32 || BK == 64, "swizzles below");
+  static_assert(BK == 64 || BK == 128, "swizzles below; rows of a stage are whole cache lines");
   static_assert(STAGES >= 2 && STAGES <= 5, "waits below");
 };
 
@@ -157,17 +188,34 @@ __device__ __forceinline__ int mmajor_swz(int k) {
   return 0;
 }
 
+// At most N of this wave's loads to LDS in flight and all its LDS reads done,
+// then the barrier.
 template <int N>
 __device__ __forceinline__ void mm_wait_barrier() {
-  // s_waitcnt vmcnt(N), then the barrier: the immediate carries the count
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 template <int LPS, int MAXL>
 __device__ __forceinline__ void mm_wait_stage(int later) {
-  if constexpr (MAXL >= 3) { if (later >= 3) { mm_wait_barrier<3 * LPS>(); return; } }
+  if constexpr (MAXL >= 4) { if (later >= 4) { mm_wait_barrier<4 * LPS>(); return; } }
+  if constexpr (MAXL >= 3) { if (later == 3) { mm_wait_barrier<3 * LPS>(); return; } }
   if constexpr (MAXL >= 2) { if (later == 2) { mm_wait_barrier<2 * LPS>(); return; } }
   if constexpr (MAXL >= 1) { if (later == 1) { mm_wait_barrier<LPS>(); return; } }
   mm_wait_barrier<0>();
+}
+
+// Order of the instructions since the last scheduling barrier: READS LDS reads
+// and LOADS loads spread over the first of MFMAS multiplies.
+template <int READS, int LOADS, int MFMAS>
+__device__ __forceinline__ void mm_interleave() {
+  constexpr int kSlots = MFMAS > 2 ? MFMAS - 2 : 1;   // the last two cover the reads' latency
+  constexpr int R = (READS + kSlots - 1) / kSlots, L = (LOADS + kSlots - 1) / kSlots;
+#pragma unroll
+  for (int m = 0; m < MFMAS; ++m) {
+    if (m * R < READS) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    if (m * L < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, L, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 constexpr uint32_t kMMPastEnd = 0x80000000u;   // at or past the end of every resource here
@@ -183,6 +231,10 @@ constexpr int kMMGroupM = 8;                   // m tiles walked together over a
 struct MMTile {
   int e, nt, p0, p1;   // rows [p0, p1), at most BM of them
 };
+__device__ __forceinline__ i32x2_t tr_read(const lds_s16x4_t* __restrict__ p) {
+  return __builtin_bit_cast(i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p));
+}
+
 template <int BM, int NTHR>
 __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, int rows, int E,
                                              int NT, int* sm, MMTile& t) {
@@ -259,9 +311,10 @@ __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, in
 }
 
 template <class T, int MODE, class G>
-__global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(const MMArgs a) {
+__global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
+    const uint8_t* __restrict__ Ab, const uint8_t* __restrict__ Bb, const MMArgs a) {
   constexpr int BM = G::BM, BN = G::BN, BK = G::BK, NTHR = G::kThreads, STAGES = G::STAGES;
-  constexpr int MI = G::MI, NJ = G::NJ, CPR = BK / 8;
+  constexpr int MI = G::MI, NJ = G::NJ, CPR = BK / 8, KS = BK / 16;
   constexpr int RW = BM / G::WM, CW = BN / G::WN;   // tile rows / columns per wave
   constexpr bool kAK = MODE != kModeTN;             // A is K-major
   constexpr bool kBK = MODE == kModeNT;             // B is K-major
@@ -325,8 +378,6 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(const MMArgs a)
 
   // ---- operand addresses
   const size_t esz = 2;
-  const uint8_t* Ab = static_cast<const uint8_t*>(a.A);
-  const uint8_t* Bb = static_cast<const uint8_t*>(a.B);
   const bool gather = a.slot != nullptr;
   if constexpr (MODE == kModeNT) {
     if (gather) {
@@ -443,46 +494,93 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(const MMArgs a)
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   // operand fragment of 16-k step ks at tile row / column `at` (a multiple of 32)
-  auto kmajor_frag = [&](const uint8_t* tile, int at, int ks) -> uint4 {
+  auto kmajor_frag = [&](const uint8_t* tile, int at, int ks) -> frag_t {
     const int row = at + l32;
-    return *reinterpret_cast<const uint4*>(
+    return *reinterpret_cast<const frag_t*>(
         tile + (row * CPR + ((2 * ks + hf) ^ kmajor_swz<CPR>(row))) * 16);
   };
-  auto mmajor_frag = [&](const uint8_t* tile, int at, int ks, auto cols) -> uint4 {
+  auto mmajor_frag = [&](const uint8_t* tile, int at, int ks, auto cols) -> frag_t {
     constexpr int COLS = decltype(cols)::value;
     const int k = 16 * ks + 8 * hf + (l16 >> 2);
     const int c = (at + (lane & 16)) / 8 + ((l16 & 3) >> 1);
     const uint8_t* p = tile + (k * (COLS / 8) + (c ^ mmajor_swz<COLS>(k))) * 16 + (l16 & 1) * 8;
-    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * COLS * 2));
-    const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
-    return make_uint4(l2.x, l2.y, h2.x, h2.y);
+    const i32x2_t l2 = tr_read((const lds_s16x4_t*)(p));
+    const i32x2_t h2 = tr_read((const lds_s16x4_t*)(p + 4 * COLS * 2));
+    return frag_t{l2[0], l2[1], h2[0], h2[1]};
   };
-  auto compute = [&](const uint8_t* base) {
-    const uint8_t* at = base;
+  // fragments of 16-k step ks of the stage at `base`
+  auto read_frags = [&](const uint8_t* base, int ks, frag_t (&fa)[4], frag_t (&fb)[4]) {
     const uint8_t* bt = base + G::kASlots * 16;
 #pragma unroll
-    for (int ks = 0; ks < BK / 16; ++ks) {
-      uint4 fa[MI], fb[NJ];
+    for (int j = 0; j < NJ; ++j) {
+      if constexpr (kBK) fb[j] = kmajor_frag(bt, wn * CW + j * 32, ks);
+      else fb[j] = mmajor_frag(bt, wn * CW + j * 32, ks, std::integral_constant<int, BN>{});
+    }
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        if constexpr (kAK) fa[i] = kmajor_frag(at, wm * RW + i * 32, ks);
-        else fa[i] = mmajor_frag(at, wm * RW + i * 32, ks, std::integral_constant<int, BM>{});
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if constexpr (kBK) fb[j] = kmajor_frag(bt, wn * CW + j * 32, ks);
-        else fb[j] = mmajor_frag(bt, wn * CW + j * 32, ks, std::integral_constant<int, BN>{});
-      }
-      // C^T subtiles: a lane ends with 4 consecutive columns n of one row m
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma16<T>(fb[j], fa[i], acc[i][j]);
+    for (int i = 0; i < MI; ++i) {
+      if constexpr (kAK) fa[i] = kmajor_frag(base, wm * RW + i * 32, ks);
+      else fa[i] = mmajor_frag(base, wm * RW + i * 32, ks, std::integral_constant<int, BM>{});
     }
   };
+  // C^T subtiles: a lane ends with 4 consecutive columns n of one row m
+  auto multiply = [&](const frag_t (&fa)[4], const frag_t (&fb)[4], auto from, auto to) {
+#pragma unroll
+    for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma16<T>(fb[j], fa[i], acc[i][j]);
+  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, MI / 2> c1{};
+  constexpr std::integral_constant<int, MI> c2{};
+  // LDS reads of one step's fragments, spread over its multiplies
+  constexpr int kReads = NJ * (kBK ? 1 : 2) + MI * (kAK ? 1 : 2);
   // a wave whose rows all lie past the tile's last row has nothing to compute
   const bool live = __builtin_amdgcn_readfirstlane(wm) * RW < mrows;
+
+  // Pipeline: the fragments of a 16-k step are read from LDS while the step
+  // before it multiplies, across stages too. The one barrier of a stage stands
+  // in the middle of its last step: there every wave holds that step's fragments
+  // in registers, so the stage's buffer is free for stage st + STAGES, and the
+  // first fragments of stage st + 1 (landed by then) can be read; the multiplies
+  // issued before it run on while the waves gather. sched_group_barrier keeps
+  // LDS reads (0x100), loads (0x020) and MFMAs (0x008) interleaved in that order:
+  // left alone, the compiler sinks each read to its use.
+  auto run = [&](auto livec, int ns, int seg0) {
+    constexpr bool LIVE = decltype(livec)::value;
+    frag_t fa[2][4], fb[2][4];
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st)
+      if (st < ns) issue(st, seg0);
+    mm_wait_stage<G::kLoads, STAGES - 1>(min(STAGES - 1, ns - 1));
+    if constexpr (LIVE) read_frags(mm_lds, 0, fa[0], fb[0]);
+    auto stage = [&](int st, auto mainc) {
+      constexpr bool MAIN = decltype(mainc)::value;   // stage st + STAGES exists
+      const uint8_t* base = mm_lds + (st % STAGES) * G::kStageBytes;
+      if constexpr (LIVE) {
+#pragma unroll
+        for (int ks = 0; ks < KS - 1; ++ks) {
+          read_frags(base, ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+          multiply(fa[ks & 1], fb[ks & 1], c0, c2);
+          mm_interleave<kReads, 0, MI * NJ>();
+        }
+        multiply(fa[1], fb[1], c0, c1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (MAIN || st + 1 < ns) {
+        if constexpr (MAIN && STAGES >= 2) mm_wait_barrier<(STAGES - 2) * G::kLoads>();
+        else mm_wait_stage<G::kLoads, STAGES - 2>(min(STAGES - 2, ns - 2 - st));
+        if constexpr (MAIN) issue(st + STAGES, seg0);
+        if constexpr (LIVE) read_frags(mm_lds + ((st + 1) % STAGES) * G::kStageBytes, 0, fa[0], fb[0]);
+      }
+      if constexpr (LIVE) {
+        multiply(fa[1], fb[1], c1, c2);
+        mm_interleave<kReads, MAIN ? G::kLoads : 0, (MI - MI / 2) * NJ>();
+      }
+    };
+    int st = 0;
+    for (; st + STAGES < ns; ++st) stage(st, std::true_type{});
+    for (; st < ns; ++st) stage(st, std::false_type{});
+  };
 
   constexpr int kSegSteps = kMMSegRows / BK;
   const int seg_len = MODE == kModeTN && gather ? kSegSteps : steps;
@@ -498,104 +596,87 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(const MMArgs a)
         __syncthreads();
       }
     }
-#pragma unroll
-    for (int st = 0; st < STAGES - 1; ++st)
-      if (st < ns) issue(st, seg0);
-    for (int st = 0; st < ns; ++st) {
-      // stage st has landed once at most the later stages' loads are in flight;
-      // the barrier also ends every wave's reads of the buffer issued next
-      mm_wait_stage<G::kLoads, STAGES - 2>(min(STAGES - 2, ns - 1 - st));
-      if (st + STAGES - 1 < ns) issue(st + STAGES - 1, seg0);
-      if (live) compute(mm_lds + (st % STAGES) * G::kStageBytes);
-    }
+    if (live) run(std::true_type{}, ns, seg0);
+    else run(std::false_type{}, ns, seg0);
   }
-  if (!live) return;
 
-  // ---- epilogue: lane (l32, hf) holds row l32 and columns 8q + 4hf + [0, 4) of
-  // each 32 x 32 subtile
+  // ---- epilogue. Lane (l32, hf) holds row l32 and columns 8q + 4hf + [0, 4) of
+  // each 32 x 32 subtile. 32 rows of a wave's columns at a time pass through a
+  // float32 area of LDS that is the wave's own, from where 8 columns of a row go
+  // to a lane: whole row pieces are read and written (bias, residual, z, C), and
+  // the activation's code stands once instead of once per accumulator.
+  __syncthreads();   // the stages are read
+  if (!live) return;
+  constexpr int kRowF = CW + 4;   // floats per row of the area; + 4: banks
+  float* area = reinterpret_cast<float*>(mm_lds) + wvu * 32 * kRowF;
   const int out_w = swiglu ? half_n : a.ndim;
-  const int nj_out = swiglu ? NJ / 2 : NJ;
-#pragma unroll
+  const int wcols = swiglu ? CW / 2 : CW;        // output columns of the wave
+  const int col0 = n0 + wn * wcols;
+  const int per_row = wcols / 8;                 // lanes per row
   for (int i = 0; i < MI; ++i) {
-    const int row = wm * RW + i * 32 + l32;
-    if (row >= mrows) continue;
-    const size_t p = static_cast<size_t>(m0) + row;
-    size_t cp = p;
-    if (MODE == kModeTN)
-      cp = (static_cast<size_t>(e) * a.splits + split) * a.mdim + p;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      if (j >= nj_out) continue;
+    for (int x = 0; x < MI; ++x)
+      if (x == i) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = n0 + (swiglu ? wn * (CW / 2) : wn * CW) + j * 32 + q * 8 + hf * 4;
-        if (col >= out_w) continue;
-        float v[4];
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] = acc[i][j][q * 4 + t];
-        if constexpr (MODE == kModeNT) {
-          if (a.bias) {
-            const uint2 bw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.bias) + col);
-            float b[4];
-            unpack2<T>(bw.x, b[0], b[1]);
-            unpack2<T>(bw.y, b[2], b[3]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) v[t] += b[t];
-          }
-          uint16_t* zrow = static_cast<uint16_t*>(a.z);
-          if (zrow) {
-            zrow += p * a.ndim;
-            *reinterpret_cast<uint2*>(zrow + col) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-          }
-          if (swiglu) {
-            if constexpr (NJ >= 2) {
-              float u[4];
-#pragma unroll
-              for (int t = 0; t < 4; ++t) u[t] = acc[i][(j + NJ / 2) % NJ][q * 4 + t];
-              if (a.bias) {
-                const uint2 bw = *reinterpret_cast<const uint2*>(
-                    static_cast<const uint16_t*>(a.bias) + half_n + col);
-                float b[4];
-                unpack2<T>(bw.x, b[0], b[1]);
-                unpack2<T>(bw.y, b[2], b[3]);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) u[t] += b[t];
-              }
-              if (zrow)
-                *reinterpret_cast<uint2*>(zrow + half_n + col) =
-                    make_uint2(pack2<T>(u[0], u[1]), pack2<T>(u[2], u[3]));
-#pragma unroll
-              for (int t = 0; t < 4; ++t) v[t] = act_f32(v[t], 2) * u[t];
-            }
-          } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) v[t] = act_f32(v[t], a.act);
-          }
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4_t*>(area + l32 * kRowF + j * 32 + q * 8 + hf * 4) =
+                f32x4_t{acc[x][j][q * 4], acc[x][j][q * 4 + 1], acc[x][j][q * 4 + 2],
+                        acc[x][j][q * 4 + 3]};
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    for (int it = lane; it < 32 * per_row; it += kWave) {
+      const int r = it / per_row, c = (it - r * per_row) * 8;
+      const int row = wm * RW + i * 32 + r, col = col0 + c;
+      if (row >= mrows || col >= out_w) continue;
+      size_t p = static_cast<size_t>(m0) + row;
+      if (MODE == kModeTN) p += (static_cast<size_t>(e) * a.splits + split) * a.mdim;
+      float v[8];
+      mm_area8(area + r * kRowF + c, v);
+      if constexpr (MODE == kModeNT) {
+        if (a.bias) mm_add8<T>(static_cast<const uint16_t*>(a.bias) + col, v);
+        uint16_t* zp = static_cast<uint16_t*>(a.z);
+        if (zp) {
+          zp += p * a.ndim + col;
+          mm_store8<T>(zp, v);
         }
-        const size_t at = cp * out_w + col;
-        if (MODE == kModeNT && a.residual) {
-          if (a.c_f32) {
-            const float4 r4 = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at);
-            v[0] += r4.x;
-            v[1] += r4.y;
-            v[2] += r4.z;
-            v[3] += r4.w;
-          } else {
-            const uint2 rw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + at);
-            float r[4];
-            unpack2<T>(rw.x, r[0], r[1]);
-            unpack2<T>(rw.y, r[2], r[3]);
+        if (swiglu) {
+          float u[8];
+          mm_area8(area + r * kRowF + CW / 2 + c, u);
+          if (a.bias) mm_add8<T>(static_cast<const uint16_t*>(a.bias) + half_n + col, u);
+          if (zp) mm_store8<T>(zp + half_n, u);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) v[t] += r[t];
-          }
+          for (int t = 0; t < 8; ++t) v[t] = act_f32(v[t], 2) * u[t];
+        } else if (a.act != 0) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[t] = act_f32(v[t], a.act);
         }
-        if (a.c_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.C) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.C) + at) =
-              make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+      }
+      const size_t at = p * out_w + col;
+      if (MODE == kModeNT && a.residual) {
+        if (a.c_f32) {
+          float w[8];
+          mm_area8(static_cast<const float*>(a.residual) + at, w);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[t] += w[t];
+        } else {
+          mm_add8<T>(static_cast<const uint16_t*>(a.residual) + at, v);
+        }
+      }
+      if (a.c_f32) {
+        f32x4_t* cp = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.C) + at);
+        cp[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+        cp[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+      } else {
+        mm_store8<T>(static_cast<uint16_t*>(a.C) + at, v);
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 }
 

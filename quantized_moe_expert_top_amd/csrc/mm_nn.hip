@@ -3,11 +3,22 @@
 #include "mm_launch.h"
 
 namespace moe {
+namespace {
 
-using NNMid = MMGeom<128, 128, 2, 2, 64, 2, 2>;
+template <class T>
+hipError_t launch(const MMArgs& a, hipStream_t s) {
+  switch (mm_pick_rows(a.rows, a.offsets ? a.E : 0, a.ndim, a.kdim)) {
+    case 0: return mm_launch<T, kModeNN, MMBig>(a, s);
+    case 1: return mm_launch<T, kModeNN, MMMid>(a, s);
+    case 2: return mm_launch<T, kModeNN, MMWide>(a, s);
+    default: return mm_launch<T, kModeNN, MMSmall>(a, s);
+  }
+}
+
+}  // namespace
 
 hipError_t launch_mm_nn(const MMArgs& a, bool fp16, hipStream_t s) {
-  return fp16 ? mm_launch<fp16_tag, kModeNN, NNMid>(a, s) : mm_launch<bf16_tag, kModeNN, NNMid>(a, s);
+  return fp16 ? launch<fp16_tag>(a, s) : launch<bf16_tag>(a, s);
 }
 
 }  // namespace moe

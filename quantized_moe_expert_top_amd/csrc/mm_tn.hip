@@ -3,24 +3,52 @@
 #include "mm_launch.h"
 
 namespace moe {
+namespace {
 
-using TNMid = MMGeom<128, 128, 2, 2, 64, 2, 2>;
-
-// Parts an expert's rows are cut into: where the output tiles alone leave CUs
-// idle, the contraction is split (each part a float32 product in the
-// workspace, added in order), down to parts of four stages.
-int mm_tn_splits(int rows, int E, int mdim, int ndim) {
-  const long long tiles = static_cast<long long>(E) * ((mdim + TNMid::BM - 1) / TNMid::BM) *
-                          ((ndim + TNMid::BN - 1) / TNMid::BN);
-  const long long most = rows / E / (4 * TNMid::BK);
-  long long s = 512 / tiles;
-  if (s > most) s = most;
-  if (s > 32) s = 32;
-  return s < 1 ? 1 : static_cast<int>(s);
+// The geometry (Big, Mid or Small) and the number of parts that an expert's rows
+// are cut into: where the output tiles alone leave CUs idle the contraction is
+// split, each part a float32 product in the workspace, added in order. A part
+// costs its bytes: written, read and the sum written at about 4 TB/s.
+struct TNPlan {
+  int geom, splits;
+};
+TNPlan plan(int rows, int E, int mdim, int ndim) {
+  TNPlan best = {0, 1};
+  double at = 1e300;
+  const double stages = (static_cast<double>(rows) / E + 63) / 64;
+  const double out_bytes = 4.0 * E * mdim * ndim;
+  for (int i = 0; i < 4; ++i) {
+    if (i == 2) continue;
+    const MMCost& c = kMMCost[i];
+    const double tiles = static_cast<double>(E) * ((mdim + c.bm - 1) / c.bm) *
+                         ((ndim + c.bn - 1) / c.bn);
+    for (int s = 1; s <= 32 && (s == 1 || stages >= 4.0 * s); s *= 2) {
+      double cost = mm_cost(c, tiles * s, stages / s);
+      if (s > 1) cost += 4.0 + out_bytes * (2 * s + 1) / 4e6;
+      if (cost < at) {
+        at = cost;
+        best = {i, s};
+      }
+    }
+  }
+  return best;
 }
 
+template <class T>
+hipError_t launch(const MMArgs& a, hipStream_t s) {
+  switch (plan(a.rows, a.E, a.mdim, a.ndim).geom) {
+    case 0: return mm_launch<T, kModeTN, MMBig>(a, s);
+    case 1: return mm_launch<T, kModeTN, MMMid>(a, s);
+    default: return mm_launch<T, kModeTN, MMSmall>(a, s);
+  }
+}
+
+}  // namespace
+
+int mm_tn_splits(int rows, int E, int mdim, int ndim) { return plan(rows, E, mdim, ndim).splits; }
+
 hipError_t launch_mm_tn(const MMArgs& a, bool fp16, hipStream_t s) {
-  return fp16 ? mm_launch<fp16_tag, kModeTN, TNMid>(a, s) : mm_launch<bf16_tag, kModeTN, TNMid>(a, s);
+  return fp16 ? launch<fp16_tag>(a, s) : launch<bf16_tag>(a, s);
 }
 
 }  // namespace moe
