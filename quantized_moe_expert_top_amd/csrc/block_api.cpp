@@ -65,6 +65,30 @@ moe_status check_gather(const moe_mm_shape* s, const int32_t* sorted_slot) {
   return MOE_OK;
 }
 
+// Arrays of a call: no output may overlap an input or another output.
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+  bool out;
+};
+template <int N>
+moe_status check_overlap(const Span (&s)[N]) {
+  for (int i = 0; i < N; ++i) {
+    if (!s[i].out || !s[i].p || !s[i].bytes) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), b = a + s[i].bytes;
+    for (int j = 0; j < N; ++j) {
+      if (j == i || (s[j].out && j < i) || !s[j].p || !s[j].bytes) continue;
+      const uintptr_t c = reinterpret_cast<uintptr_t>(s[j].p), d = c + s[j].bytes;
+      if (a < d && c < b) return fail(MOE_EINVAL, "%s overlaps %s in memory", s[i].name, s[j].name);
+    }
+  }
+  return MOE_OK;
+}
+size_t values(int64_t rows, int64_t cols, int type) {
+  return static_cast<size_t>(rows) * cols * (type == MOE_F32 ? 4 : 2);
+}
+
 moe::MMArgs mm_args(const moe_mm_shape* s, const int32_t* offsets, const int32_t* slot) {
   moe::MMArgs a = {};
   a.offsets = offsets;
@@ -150,6 +174,14 @@ moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* 
   REQUIRE_PTR(y);
   if (z) REQUIRE_PTR(z);
   if ((st = check_gather(shape, sorted_slot))) return st;
+  const int t = shape->dtype;
+  if ((st = check_overlap({{"y", y, values(shape->rows, out_width(shape), y_dtype), true},
+                           {"z", z, values(shape->rows, shape->N, t), true},
+                           {"x", x, values(sorted_slot ? shape->x_rows : shape->rows, shape->K, t), false},
+                           {"w", w, shape->E * values(shape->N, shape->K, t), false},
+                           {"expert_offsets", expert_offsets, (shape->E + 1) * size_t{4}, false},
+                           {"sorted_slot", sorted_slot, shape->rows * size_t{4}, false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   moe::MMArgs a = mm_args(shape, expert_offsets, sorted_slot);
   a.A = x;
@@ -198,6 +230,18 @@ moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy, co
       return fail(MOE_EWORKSPACE, "grouped backward workspace %zu < %zu bytes", ws_bytes, need.total);
     REQUIRE_PTR(ws);
   }
+  const int t = shape->dtype;
+  const int64_t rows = shape->rows;
+  if ((st = check_overlap({{"dx", dx, values(rows, shape->K, dx_dtype), true},
+                           {"dw", dw, shape->E * values(shape->N, shape->K, dw_dtype), true},
+                           {"ws", ws, need.total, true},
+                           {"dy", dy, values(rows, out_width(shape), t), false},
+                           {"x", x, values(sorted_slot ? shape->x_rows : rows, shape->K, t), false},
+                           {"w", w, shape->E * values(shape->N, shape->K, t), false},
+                           {"z", z, values(rows, shape->N, t), false},
+                           {"expert_offsets", expert_offsets, (shape->E + 1) * size_t{4}, false},
+                           {"sorted_slot", sorted_slot, rows * size_t{4}, false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -226,6 +270,15 @@ moe_status moe_linear(const moe_mm_shape* shape, const void* x, const void* w, c
   if (bias) REQUIRE_PTR(bias);
   if (residual) REQUIRE_PTR(residual);
   if (z) REQUIRE_PTR(z);
+  const int t = shape->dtype;
+  const size_t y_bytes = values(shape->rows, out_width(shape), y_dtype);
+  if ((st = check_overlap({{"y", y, y_bytes, true},
+                           {"z", z, values(shape->rows, shape->N, t), true},
+                           {"x", x, values(shape->rows, shape->K, t), false},
+                           {"w", w, values(shape->N, shape->K, t), false},
+                           {"bias", bias, values(1, shape->N, t), false},
+                           {"residual", residual == y ? nullptr : residual, y_bytes, false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   moe::MMArgs a = mm_args(shape, nullptr, nullptr);
   a.A = x;
@@ -273,6 +326,17 @@ moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_
       return fail(MOE_EWORKSPACE, "linear backward workspace %zu < %zu bytes", ws_bytes, need.total);
     REQUIRE_PTR(ws);
   }
+  const int t = shape->dtype;
+  const int64_t rows = shape->rows;
+  if ((st = check_overlap({{"dx", dx, values(rows, shape->K, dx_dtype), true},
+                           {"dw", dw, values(shape->N, shape->K, dw_dtype), true},
+                           {"dbias", dbias, values(1, shape->N, dw_dtype), true},
+                           {"ws", ws, need.total, true},
+                           {"dy", dy, values(rows, out_width(shape), dy_dtype), false},
+                           {"x", x, values(rows, shape->K, t), false},
+                           {"w", w, values(shape->N, shape->K, t), false},
+                           {"z", z, values(rows, shape->N, t), false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -316,6 +380,10 @@ static moe_status check_norm(const moe_norm_shape* s) {
   return MOE_OK;
 }
 
+static size_t gate_bytes(const moe_norm_shape* s) {
+  return values(s->gate == MOE_GATE_CHANNEL ? 1 : s->T, s->gate == MOE_GATE_TOKEN ? 1 : s->H, s->dtype);
+}
+
 static moe::NormArgs norm_args(const moe_norm_shape* s) {
   moe::NormArgs a = {};
   a.T = s->T;
@@ -345,6 +413,16 @@ moe_status moe_block_norm(const moe_norm_shape* shape, const void* r, const void
   if (w_pre) REQUIRE_PTR(w_pre);
   if (r_out) REQUIRE_PTR(r_out);
   if (h) REQUIRE_PTR(h);
+  const int64_t T = shape->T, H = shape->H;
+  const int t = shape->dtype;
+  if ((st = check_overlap({{"r_out", r_out, values(T, H, shape->r_dtype), true},
+                           {"h", h, values(T, H, t), true},
+                           {"r", r, values(T, H, shape->r_dtype), false},
+                           {"y", y, values(T, H, shape->y_dtype), false},
+                           {"w_post", w_post, values(1, H, t), false},
+                           {"w_pre", w_pre, values(1, H, t), false},
+                           {"gate", shape->gate ? gate : nullptr, gate_bytes(shape), false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   moe::NormArgs a = norm_args(shape);
   a.r = r;
@@ -403,6 +481,22 @@ moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* r_ou
       return fail(MOE_EWORKSPACE, "block norm backward workspace %zu < %zu bytes", ws_bytes, need);
     REQUIRE_PTR(ws);
   }
+  const int64_t H = shape->H;
+  const int t = shape->dtype;
+  if ((st = check_overlap({{"dr", dr, values(T, H, shape->r_dtype), true},
+                           {"dy", dy, values(T, H, shape->y_dtype), true},
+                           {"dw_post", dw_post, values(1, H, MOE_F32), true},
+                           {"dw_pre", dw_pre, values(1, H, MOE_F32), true},
+                           {"dgate", dgate, gate_bytes(shape) * (gk == MOE_GATE_ELEMENT ? 1 : 2), true},
+                           {"ws", sums ? ws : nullptr, need, true},
+                           {"r_out", dh ? r_out : nullptr, values(T, H, shape->r_dtype), false},
+                           {"dr_out", dr_out, values(T, H, shape->r_dtype), false},
+                           {"dh", dh, values(T, H, t), false},
+                           {"y", y, values(T, H, shape->y_dtype), false},
+                           {"w_post", w_post, values(1, H, t), false},
+                           {"w_pre", w_pre, values(1, H, t), false},
+                           {"gate", gk ? gate : nullptr, gate_bytes(shape), false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   moe::NormArgs a = norm_args(shape);
   a.r = r_out;
@@ -445,6 +539,16 @@ moe_status moe_combine_backward(const float* dout, const float* y, const int32_t
   if (dtopk_w) REQUIRE_PTR(dtopk_w);
   if (dlogits) REQUIRE_PTR(dlogits);
   moe_status st;
+  const int64_t R = static_cast<int64_t>(T) * k;
+  if ((st = check_overlap({{"dy", dy, values(R, H, dy_dtype), true},
+                           {"dtopk_w", dtopk_w, values(T, k, MOE_F32), true},
+                           {"dlogits", dlogits, values(T, E, MOE_F32), true},
+                           {"dout", dout, values(T, H, MOE_F32), false},
+                           {"y", dtopk_w || dlogits ? y : nullptr, values(R, H, MOE_F32), false},
+                           {"slot_pos", slot_pos, values(R, 1, MOE_F32), false},
+                           {"topk_w", topk_w, values(R, 1, MOE_F32), false},
+                           {"topk_ids", dlogits ? topk_ids : nullptr, values(R, 1, MOE_F32), false}})))
+    return st;
   if ((st = check_device()) != MOE_OK) return st;
   return launched(moe::launch_combine_backward(dout, y, slot_pos, topk_ids, topk_w, T, H, E, k, dy,
                                                dy ? dy_dtype : MOE_F32, dtopk_w, dlogits,

@@ -1,5 +1,8 @@
 // Host side of the tile products: choice of a geometry, grid sizes, launch.
 #pragma once
+#include <atomic>
+
+#include "api_util.h"
 #include "mm.h"
 
 namespace moe {
@@ -71,9 +74,18 @@ hipError_t mm_launch(MMArgs a, hipStream_t s) {
   const long long grid = (tiles + 7) / 8 * 8;
   if (grid == 0) return hipSuccess;
   if (grid >= (1LL << 31)) return hipErrorInvalidConfiguration;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&mm_kernel<T, MODE, G>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
+  // the attribute is set once per device (threads that race set it twice)
+  static std::atomic<bool> ready[moe_api::kMaxDevices];
+  int dev = -1;
+  hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= moe_api::kMaxDevices) return hipErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&mm_kernel<T, MODE, G>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
+    if (e != hipSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
+  }
   hipLaunchKernelGGL((mm_kernel<T, MODE, G>), dim3(static_cast<unsigned>(grid)),
                      dim3(G::kThreads), G::kLds, s,
                      static_cast<const uint8_t*>(a.A), static_cast<const uint8_t*>(a.B), a);

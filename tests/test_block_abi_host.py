@@ -22,6 +22,13 @@ pytestmark = pytest.mark.skipif(LIB is None, reason="libmoe.so not built")
 
 A = 0x10000          # a 16-byte aligned stand-in address, never dereferenced on the host
 MIS = 0x10008        # misaligned
+
+
+def place(*args):
+    """A place of its own for every operand that stands at A (2^32 bytes apart)."""
+    return [(i + 1) << 32 if v == A else v for i, v in enumerate(args)]
+
+
 BIG = 1 << 40        # a workspace size no check refuses
 NO_GPU = not torch.cuda.is_available()
 OK, EINVAL, ESHAPE, EALIGN, EWS, EDEV = 0, 1, 2, 3, 4, 6
@@ -51,19 +58,21 @@ BAD_SHAPES = [
 
 
 def grouped(s, x=A, w=A, off=A, slot=None, z=None, y=A, yt=BF):
-    return LIB.moe_grouped_mm(ctypes.byref(s) if s else None, x, w, off, slot, z, y, yt, None)
+    return LIB.moe_grouped_mm(ctypes.byref(s) if s else None, *place(x, w, off, slot, z, y), yt, None)
 
 
 def grouped_bwd(s, dy=A, x=A, w=A, z=None, off=A, slot=None, dx=A, dxt=BF, dw=A, dwt=BF, ws=A, n=BIG):
+    dy, x, w, z, off, slot, dx, dw, ws = place(dy, x, w, z, off, slot, dx, dw, ws)
     return LIB.moe_grouped_mm_backward(ctypes.byref(s) if s else None, dy, x, w, z, off, slot, dx,
                                        dxt, dw, dwt, ws, n, None)
 
 
 def lin(s, x=A, w=A, bias=None, res=None, z=None, y=A, yt=BF):
-    return LIB.moe_linear(ctypes.byref(s) if s else None, x, w, bias, res, z, y, yt, None)
+    return LIB.moe_linear(ctypes.byref(s) if s else None, *place(x, w, bias, res, z, y), yt, None)
 
 
 def lin_bwd(s, dy=A, dyt=BF, x=A, w=A, z=None, dx=A, dxt=BF, dw=A, db=A, dwt=BF, ws=A, n=BIG):
+    dy, x, w, z, dx, dw, db, ws = place(dy, x, w, z, dx, dw, db, ws)
     return LIB.moe_linear_backward(ctypes.byref(s) if s else None, dy, dyt, x, w, z, dx, dxt, dw,
                                    db, dwt, ws, n, None)
 
@@ -162,12 +171,13 @@ def norm(T=4, H=64, dtype=BF, r=BF, y=F32, gate=0, scale=1.0, eps=1e-6):
 
 
 def nf(s, r=A, y=A, wp=A, g=None, wn=A, ro=A, h=A):
-    return LIB.moe_block_norm(ctypes.byref(s) if s else None, r, y, wp, g, wn, ro, h, None)
+    return LIB.moe_block_norm(ctypes.byref(s) if s else None, *place(r, y, wp, g, wn, ro, h), None)
 
 
 def nb(s, r=A, dro=A, dh=A, y=A, wp=A, g=None, wn=A, dr=A, dy=A, dwp=A, dwn=A, dg=None, ws=A, n=BIG):
-    return LIB.moe_block_norm_backward(ctypes.byref(s) if s else None, r, dro, dh, y, wp, g, wn, dr,
-                                       dy, dwp, dwn, dg, ws, n, None)
+    return LIB.moe_block_norm_backward(ctypes.byref(s) if s else None,
+                                       *place(r, dro, dh, y, wp, g, wn, dr, dy, dwp, dwn, dg, ws),
+                                       n, None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -220,6 +230,7 @@ def test_norm_backward_refusals():
 
 
 def cb(dout=A, y=A, pos=A, ids=A, w=A, T=4, H=64, E=8, k=2, dy=A, dyt=BF, dw=A, dl=A):
+    dout, y, pos, ids, w, dy, dw, dl = place(dout, y, pos, ids, w, dy, dw, dl)
     return LIB.moe_combine_backward(dout, y, pos, ids, w, T, H, E, k, dy, dyt, dw, dl, None)
 
 
@@ -288,21 +299,33 @@ def test_binding_refuses_shapes_types_and_layouts():
         pytest.fail(f"call {i} was not refused")
 
 
-def test_binding_refuses_overlaps():
+def test_overlaps_refused():
+    """An output that overlaps an input or another output, by a byte or whole."""
     import quantized_moe_expert_top_amd as moe
     off = torch.zeros(2, dtype=torch.int32)
     buf = _t((16, 64))
     w = _t((64, 64))
-    with pytest.raises(ValueError, match="overlaps"):
-        moe.linear(buf[:8], w, buf[4:12])
-    with pytest.raises(ValueError, match="overlaps"):
-        moe.linear(buf[:8], w, buf[8:], residual=buf[7:15])      # y shifted by a row
-    with pytest.raises(ValueError, match="overlaps"):
-        moe.grouped_mm(buf[:8], w[None], off, _t((8, 64)), z=w[:8])
-    with pytest.raises(ValueError, match="overlaps"):
-        moe.block_norm(buf, y=_t((16, 64)), r_out=buf)
-    with pytest.raises(ValueError, match="overlaps"):
-        moe.linear_backward(buf[:8], buf[8:], w, dx=_t((8, 64)), dw=w)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    calls = [
+        lambda: moe.linear(buf[:8], w, buf[4:12]),
+        lambda: moe.linear(buf[:8], w, buf[8:], residual=buf[7:15]),       # shifted by a row
+        lambda: moe.linear(buf[:8], w, buf[8:], z=buf[8:]),
+        lambda: moe.grouped_mm(buf[:8], w[None], off, _t((8, 64)), z=w[:8]),
+        lambda: moe.block_norm(buf, y=_t((16, 64)), r_out=buf),
+        lambda: moe.linear_backward(buf[:8], buf[8:], w, dx=_t((8, 64)), dw=w, ws=ws),
+        lambda: moe.grouped_mm_backward(buf[:8], buf[8:], w[None], off, dx=buf[1:9], ws=ws),
+        lambda: moe.linear_backward(buf[:8], buf[8:], w, dx=_t((8, 64)),
+                                    ws=w.view(torch.uint8).reshape(-1)),
+        lambda: moe.block_norm_backward(buf, buf, dr_out=_t((16, 64)), dh=_t((16, 64)), w_pre=w[0]),
+    ]
+    for i, f in enumerate(calls):
+        with pytest.raises(moe.MoeError) as ei:
+            f()
+        assert ei.value.status == EINVAL and "overlaps" in str(ei.value), i
+    if NO_GPU:
+        with pytest.raises(moe.MoeError) as ei:       # the residual may be y itself
+            moe.linear(buf[:8], w, buf[8:], residual=buf[8:])
+        assert ei.value.status == EDEV
 
 
 def test_binding_raises_library_errors():
