@@ -12,23 +12,25 @@ using MMMid = MMGeom<128, 128, 2, 2, 64, 2, 2>;    // 4 waves, two blocks per CU
 using MMWide = MMGeom<64, 128, 2, 4, 64, 3, 4>;    // 8 waves, two blocks per CU
 using MMSmall = MMGeom<64, 64, 2, 2, 64, 4, 2>;    // 4 waves, two blocks per CU
 
-// What a geometry costs: rounds of resident blocks, each of `stage` us per 64-k
-// stage plus `fixed` us for its first loads and its epilogue. Fitted to timings
-// of NT products on one MI355X (us for Big / Mid / Wide / Small):
-//   8192 x 4096 x 7168            372 / 462 / -   / -
-//   4096 x 2048 x 1536             41 /  30 /  36 /  42
-//   512 x 2048 x 768                - / 10.7 / 8.1 / 6.4
-//   grouped, 128 experts, 32768 rows x 1536 x 2048   311 / 324 / 366 / 420
-//   grouped, 128 experts,  4096 rows x 1536 x 2048   200 / 189 / 166 / 163
-//   grouped, 14 of 128 experts, 16 rows x 1536 x 2048  30 / 22 / 15.7 / 17.2
+// What a geometry costs, in us on one MI355X: a round of resident blocks takes
+// `s1`, `s2` or `s3` per 64-k stage with 64, 256 or `slots` blocks at work (fewer
+// blocks, more of the caches' rate for each; between them in proportion), and
+// `full` (a full round) or `part` (the last one) for first loads and epilogues.
+// Fitted; what the fit says and, in brackets, what was timed:
+//   NT  8192 x 4096 x 7168   Big 385 (376)   Mid 466 (462)
+//       4096 x 2048 x 1536   Big 43 (38)     Mid 32 (28)    Wide 44 (36)    Small 59 (42)
+//       512 x 2048 x 768     Mid 11 (10.7)   Wide 7.8 (8.1) Small 6.3 (6.5)
+//       grouped, 128 experts, 32768 x 1536 x 2048   Big 297 (306)   Mid 302 (320)
+//       grouped, 128 experts, 32768 x 2048 x 768    Big 172 (205)   Mid 205 (214)
+//   TN  1536 x 2048 x 4096   Big 83 (85)     Mid 45 (41)    Small 52 (50)
 struct MMCost {
   int bm, bn, slots;
-  double stage, fixed;
+  double s1, s2, s3, full, part;
 };
-constexpr MMCost kMMCost[4] = {{256, 256, 256, 1.60, 8.0},
-                               {128, 128, 512, 1.00, 6.0},
-                               {64, 128, 512, 0.62, 3.0},
-                               {64, 64, 512, 0.36, 2.5}};
+constexpr MMCost kMMBigCost = {256, 256, 256, 1.12, 1.64, 1.64, 9.0, 9.0};
+constexpr MMCost kMMMidCost = {128, 128, 512, 0.57, 0.65, 0.96, 9.0, 4.0};
+constexpr MMCost kMMWideCost = {64, 128, 512, 0.30, 0.36, 0.65, 6.5, 3.8};
+constexpr MMCost kMMSmallCost = {64, 64, 512, 0.20, 0.23, 0.40, 5.0, 3.5};
 
 // m tiles of row blocks: of `rows` rows in one block (E = 0), or spread over E
 // experts, where about half a tile per expert in use is left over and none has
@@ -39,15 +41,24 @@ inline double mm_row_tiles(int bm, int rows, int E) {
   return n > act ? n : act;
 }
 inline double mm_cost(const MMCost& c, double tiles, double stages) {
-  const double rounds = tiles <= c.slots ? 1.0 : __builtin_ceil(tiles / c.slots);
-  return rounds * (stages * c.stage + c.fixed);
+  const double full = __builtin_floor(tiles / c.slots), rem = tiles - full * c.slots;
+  double cost = full * (stages * c.s3 + c.full);
+  if (rem > 0) {
+    const double s = rem <= 64    ? c.s1
+                     : rem <= 256 ? c.s1 + (c.s2 - c.s1) * (rem - 64) / 192
+                                  : c.s2 + (c.s3 - c.s2) * (rem - 256) / (c.slots - 256);
+    cost += stages * s + c.part;
+  }
+  return cost;
 }
-// Index into kMMCost of the cheapest geometry for row-grouped products (NT, NN).
+// The cheapest geometry for row-grouped products (NT, NN): 0 Big, 1 Mid, 2 Wide,
+// 3 Small.
 inline int mm_pick_rows(int rows, int E, int ndim, int kdim) {
+  const MMCost* const table[4] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost};
   int best = 0;
   double at = 1e300;
   for (int i = 0; i < 4; ++i) {
-    const MMCost& c = kMMCost[i];
+    const MMCost& c = *table[i];
     const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * ((ndim + c.bn - 1) / c.bn),
                                 (kdim + 63) / 64);
     if (cost < at) {
@@ -58,6 +69,12 @@ inline int mm_pick_rows(int rows, int E, int ndim, int kdim) {
   return best;
 }
 
+// Results of more than the L2s' 32 MB go past them (see mm_put16).
+inline void mm_set_stream(MMArgs& a, long long values) {
+  const long long bytes = values * (a.c_f32 ? 4 : 2) + (a.z ? 2LL * a.rows * a.ndim : 0);
+  a.stream_out = bytes > (32LL << 20);
+}
+
 template <class T, int MODE, class G>
 hipError_t mm_launch(MMArgs a, hipStream_t s) {
   long long tiles;
@@ -66,7 +83,9 @@ hipError_t mm_launch(MMArgs a, hipStream_t s) {
   if (MODE == kModeTN) {
     a.mt = (a.mdim + G::BM - 1) / G::BM;
     tiles = static_cast<long long>(a.E) * a.splits * a.mt * a.nt;
+    mm_set_stream(a, static_cast<long long>(a.E) * a.splits * a.mdim * a.ndim);
   } else {
+    mm_set_stream(a, static_cast<long long>(a.rows) * (swiglu ? a.ndim / 2 : a.ndim));
     // an upper bound over all ways to cut the rows: a partial tile per expert
     const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
     tiles = (a.rows / G::BM + partial) * a.nt;

@@ -294,7 +294,7 @@ def test_grouped_backward(i, act):
 
 def test_grouped_backward_long_gather():
     """More rows of one expert than the kernel holds source indices for at a time
-    (2048), rows of other experts before and behind."""
+    (1024), rows of other experts before and behind."""
     import quantized_moe_expert_top_amd as moe
     sizes, K, N, topk = [3, 4500, 0, 10, 2048], 72, 80, 3
     off = _offsets(sizes)
