@@ -438,7 +438,7 @@ moe_status moe_block_norm(const moe_norm_shape* shape, const void* r, const void
 
 size_t moe_block_norm_backward_workspace(int32_t T, int32_t H) {
   if (T < 0 || H < 8 || H % 8 || H > MOE_NORM_MAX_H) return 0;
-  return align256(static_cast<size_t>(moe::norm_backward_blocks(T, H)) * 3 * H * 4);
+  return align256(static_cast<size_t>(moe::norm_backward_blocks(T, H)) * 2 * H * 4);
 }
 
 moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* r_out,

@@ -15,20 +15,26 @@ namespace {
 
 constexpr int kMaxPicks = 32;
 
-template <int DY>   // 0 bf16, 1 fp16, 2 float32
-__device__ __forceinline__ void store_dy(void* dy, size_t at, const float4& a, const float4& b) {
+// DY: 0 bf16, 1 fp16, 2 float32. STREAM: past the caches (see mm_put16), where dy
+// takes more than the L2s' 32 MB.
+template <bool STREAM>
+__device__ __forceinline__ void put16(i32x4_t w, void* p) {
+  if constexpr (STREAM) __builtin_nontemporal_store(w, static_cast<i32x4_t*>(p));
+  else *static_cast<i32x4_t*>(p) = w;
+}
+template <int DY, bool STREAM>
+__device__ __forceinline__ void store_dy(void* dy, size_t at, const float (&v)[8]) {
   if constexpr (DY == 2) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(dy) + at);
-    q[0] = a;
-    q[1] = b;
+    float* q = static_cast<float*>(dy) + at;
+    put16<STREAM>(__builtin_bit_cast(i32x4_t, f32x4_t{v[0], v[1], v[2], v[3]}), q);
+    put16<STREAM>(__builtin_bit_cast(i32x4_t, f32x4_t{v[4], v[5], v[6], v[7]}), q + 4);
   } else {
     using T = typename std::conditional<DY == 0, bf16_tag, fp16_tag>::type;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dy) + at) =
-        make_uint4(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w), pack2<T>(b.x, b.y), pack2<T>(b.z, b.w));
+    put16<STREAM>(mm_pack8<T>(v), static_cast<uint16_t*>(dy) + at);
   }
 }
 
-template <int DY>
+template <int DY, bool STREAM>
 __global__ __launch_bounds__(512) void combine_backward_kernel(
     const float* __restrict__ dout, const float* __restrict__ y, const int* __restrict__ slot_pos,
     const int* __restrict__ ids, const float* __restrict__ w, int T, int H, int E, int k,
@@ -59,9 +65,11 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(
         dot += d0.x * y0.x + d0.y * y0.y + d0.z * y0.z + d0.w * y0.w + d1.x * y1.x + d1.y * y1.y +
                d1.z * y1.z + d1.w * y1.w;
       }
-      if (dy)
-        store_dy<DY>(dy, row + c * 8, make_float4(wj * d0.x, wj * d0.y, wj * d0.z, wj * d0.w),
-                     make_float4(wj * d1.x, wj * d1.y, wj * d1.z, wj * d1.w));
+      if (dy) {
+        const float v[8] = {wj * d0.x, wj * d0.y, wj * d0.z, wj * d0.w,
+                            wj * d1.x, wj * d1.y, wj * d1.z, wj * d1.w};
+        store_dy<DY, STREAM>(dy, row + c * 8, v);
+      }
     }
     if (need_dot) {
       dot = wave_sum_f32(dot);
@@ -92,12 +100,15 @@ hipError_t launch_combine_backward(const float* dout, const float* y, const int*
                                    hipStream_t s) {
   if (T == 0) return hipSuccess;
   const int threads = k > 4 ? 512 : k > 2 ? 256 : k > 1 ? 128 : 64;
-  if (dy_type == 0)
-    combine_backward_kernel<0><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
-  else if (dy_type == 1)
-    combine_backward_kernel<1><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
-  else
-    combine_backward_kernel<2><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+  const bool stream = dy && static_cast<long long>(T) * k * H * (dy_type == 2 ? 4 : 2) > (32LL << 20);
+  auto launch = [&](auto dyc) {
+    constexpr int DY = decltype(dyc)::value;
+    if (stream) combine_backward_kernel<DY, true><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+    else combine_backward_kernel<DY, false><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+  };
+  if (dy_type == 0) launch(std::integral_constant<int, 0>{});
+  else if (dy_type == 1) launch(std::integral_constant<int, 1>{});
+  else launch(std::integral_constant<int, 2>{});
   return hipGetLastError();
 }
 

@@ -39,7 +39,7 @@ struct NormArgs {
   void* dr;
   void* dy;
   void* dgate;
-  float* part;          // [blocks][3][H]: dw_pre, dw_post, dgate
+  float* part;          // [blocks][2][H]: sums over tokens
   int T, H, gate_kind;
   int r_f32, y_f32;
   float scale, eps;

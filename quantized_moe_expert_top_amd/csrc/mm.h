@@ -163,6 +163,7 @@ struct MMArgs {
   int splits;            // TN: parts of an expert's rows, each to its own C
   int nt;                // n tiles
   int mt;                // TN: m tiles
+  int xm;                // TN: m slices of an expert's tiles over the XCDs (1, 2, 4, 8), or 0
 };
 
 // Geometry of a block: BM x BN of C, WM x WN waves, K in stages of BK, STAGES of
@@ -346,18 +347,35 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
   int k_begin = 0, k_end = 0;       // TN: rows contracted over
   int split = 0;
   if constexpr (MODE == kModeTN) {
-    const int total = a.E * a.splits * a.mt * a.nt, chunk = (total + 7) / 8;
-    int tau = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-    if (static_cast<int>(blockIdx.x >> 3) >= chunk || tau >= total) return;
-    const int per_e = a.mt * a.nt;
-    const int es = tau / per_e;
-    tau -= es * per_e;
+    int es, mi, ni;
+    if (a.xm > 0) {
+      // several experts: every XCD takes a rectangle of each expert's tiles (xm
+      // slices of m by 8 / xm of n), so that experts with many rows load all XCDs
+      // alike (runs of whole experts per XCD: 394 us for 32768 rows, 8 to 1513
+      // per expert, against 314 us with 256 each)
+      const int xcd = blockIdx.x & 7, l0 = blockIdx.x >> 3;
+      const int xn = 8 / a.xm, tm = (a.mt + a.xm - 1) / a.xm, tn = (a.nt + xn - 1) / xn;
+      es = l0 / (tm * tn);
+      const int l = l0 - es * tm * tn;
+      mi = (xcd % a.xm) * tm + l % tm;
+      ni = (xcd / a.xm) * tn + l / tm;
+      if (es >= a.E * a.splits || mi >= a.mt || ni >= a.nt) return;
+    } else {
+      const int total = a.E * a.splits * a.mt * a.nt, chunk = (total + 7) / 8;
+      int tau = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+      if (static_cast<int>(blockIdx.x >> 3) >= chunk || tau >= total) return;
+      const int per_e = a.mt * a.nt;
+      es = tau / per_e;
+      tau -= es * per_e;
+      const int per = kMMGroupM * a.nt, g = tau / per, r = tau - g * per;
+      const int gm = min(kMMGroupM, a.mt - g * kMMGroupM);
+      ni = r / gm;
+      mi = g * kMMGroupM + r % gm;
+    }
     e = es / a.splits;
     split = es % a.splits;
-    const int per = kMMGroupM * a.nt, g = tau / per, r = tau - g * per;
-    const int gm = min(kMMGroupM, a.mt - g * kMMGroupM);
-    n0 = (r / gm) * BN;
-    m0 = (g * kMMGroupM + r % gm) * BM;
+    n0 = ni * BN;
+    m0 = mi * BM;
     mrows = min(BM, a.mdim - m0);
     int lo = 0, hi = a.rows;
     if (a.offsets) {

@@ -83,6 +83,21 @@ hipError_t mm_launch(MMArgs a, hipStream_t s) {
   if (MODE == kModeTN) {
     a.mt = (a.mdim + G::BM - 1) / G::BM;
     tiles = static_cast<long long>(a.E) * a.splits * a.mt * a.nt;
+    a.xm = 0;
+    if (a.E > 1) {
+      // the split of 8 XCDs that pads least, then the one that reads least: a
+      // slice reads its part of both operands
+      long long best = -1;
+      for (int xm = 1; xm <= 8; xm *= 2) {
+        const long long tm = (a.mt + xm - 1) / xm, tn = (a.nt + 8 / xm - 1) / (8 / xm);
+        const long long key = tm * tn * 1000000 + tm * G::BM + tn * G::BN;
+        if (best < 0 || key < best) {
+          best = key;
+          a.xm = xm;
+          tiles = 8 * tm * tn * a.E * a.splits;
+        }
+      }
+    }
     mm_set_stream(a, static_cast<long long>(a.E) * a.splits * a.mdim * a.ndim);
   } else {
     mm_set_stream(a, static_cast<long long>(a.rows) * (swiglu ? a.ndim / 2 : a.ndim));
