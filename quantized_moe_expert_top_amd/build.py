@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["api.cpp", "router.hip", "route.hip", "permute.hip", "w4a16.hip", "w4a8.hip",
            "w8a8.hip", "combine.hip", "telemetry.hip",
-           "block_api.cpp", "mm_nt.hip", "mm_nn.hip", "mm_tn.hip", "block_aux.hip", "norm.hip",
+           "block_api.cpp", "mm_nt.hip", "mm_nn.hip", "mm_tn.hip", "mm_pair.hip", "block_aux.hip", "norm.hip",
            "combine_backward.hip"]
 
 FLAGS = [

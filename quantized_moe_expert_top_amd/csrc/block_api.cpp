@@ -112,7 +112,7 @@ MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   if (!grouped || s->act != MOE_ACT_NONE)
     at += align256(static_cast<size_t>(s->rows) * s->N * 2);
   w.strips = at;
-  if (!grouped) at += align256(static_cast<size_t>(moe::dz_strips(s->rows)) * s->N * 4);
+  if (!grouped) at += align256(static_cast<size_t>(moe::dz_strips(s->rows, s->N, s->act)) * s->N * 4);
   w.parts = at;
   const int E = grouped ? s->E : 1, splits = moe::mm_tn_splits(s->rows, E, s->N, s->K);
   if (splits > 1) at += align256(static_cast<size_t>(E) * splits * s->N * s->K * 4);
@@ -125,30 +125,38 @@ moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* 
                              const int32_t* offsets, const int32_t* slot, void* dx, int dx_dtype,
                              void* dw, int dw_dtype, void* parts, hipStream_t st) {
   const bool fp16 = s->dtype == MOE_FP16;
+  moe::MMArgs nn = mm_args(s, offsets, nullptr);
+  nn.A = dz;
+  nn.B = w;
+  nn.C = dx;
+  nn.ndim = s->K;
+  nn.kdim = s->N;
+  nn.c_f32 = dx_dtype == MOE_F32;
+  moe::MMArgs tn = mm_args(s, offsets, slot);
+  tn.A = dz;
+  tn.B = x;
+  tn.C = dw;
+  tn.mdim = s->N;
+  tn.ndim = s->K;
+  tn.c_f32 = dw_dtype == MOE_F32;
+  if (dx && dw && s->rows > 0) {
+    const int pick = moe::mm_pair_pick(s->rows, offsets ? s->E : 0, s->N, s->K);
+    if (pick) return launched(moe::launch_mm_pair(nn, tn, pick, fp16, st), "gradient launch");
+  }
   if (dx && s->rows > 0) {
-    moe::MMArgs a = mm_args(s, offsets, nullptr);
-    a.A = dz;
-    a.B = w;
-    a.C = dx;
-    a.ndim = s->K;
-    a.kdim = s->N;
-    a.c_f32 = dx_dtype == MOE_F32;
-    const moe_status r = launched(moe::launch_mm_nn(a, fp16, st), "row gradient launch");
+    const moe_status r = launched(moe::launch_mm_nn(nn, fp16, st), "row gradient launch");
     if (r) return r;
   }
   if (dw) {
-    moe::MMArgs a = mm_args(s, offsets, slot);
-    a.A = dz;
-    a.B = x;
-    a.mdim = s->N;
-    a.ndim = s->K;
-    a.splits = moe::mm_tn_splits(s->rows, a.E, s->N, s->K);
-    a.C = a.splits > 1 ? parts : dw;
-    a.c_f32 = a.splits > 1 || dw_dtype == MOE_F32;
-    moe_status r = launched(moe::launch_mm_tn(a, fp16, st), "weight gradient launch");
+    tn.splits = moe::mm_tn_splits(s->rows, tn.E, s->N, s->K);
+    if (tn.splits > 1) {
+      tn.C = parts;
+      tn.c_f32 = 1;
+    }
+    moe_status r = launched(moe::launch_mm_tn(tn, fp16, st), "weight gradient launch");
     if (r) return r;
-    if (a.splits > 1) {
-      r = launched(moe::launch_sum_splits(static_cast<const float*>(parts), a.E, a.splits,
+    if (tn.splits > 1) {
+      r = launched(moe::launch_sum_splits(static_cast<const float*>(parts), tn.E, tn.splits,
                                           static_cast<long long>(s->N) * s->K, dw, dw_dtype, st),
                    "weight gradient sum launch");
       if (r) return r;
@@ -353,7 +361,7 @@ moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_
     if (st) return st;
   }
   if (dbias) {
-    st = launched(moe::launch_sum_parts(strips, moe::dz_strips(shape->rows), shape->N, dbias,
+    st = launched(moe::launch_sum_parts(strips, moe::dz_strips(shape->rows, shape->N, shape->act), shape->N, dbias,
                                         dw_dtype, s),
                   "bias gradient launch");
     if (st) return st;

@@ -11,12 +11,15 @@ struct MMArgs;
 hipError_t launch_mm_nt(const MMArgs& a, bool fp16, hipStream_t s);
 hipError_t launch_mm_nn(const MMArgs& a, bool fp16, hipStream_t s);
 hipError_t launch_mm_tn(const MMArgs& a, bool fp16, hipStream_t s);
+// Both gradients in one launch; pick from mm_pair_pick (E 0: no experts), 0 = apart.
+int mm_pair_pick(int rows, int E, int N, int K);
+hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, int pick, bool fp16, hipStream_t s);
 int mm_tn_splits(int rows, int E, int mdim, int ndim);
 
 // dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
-// (part [dz_strips(rows)][N], may be NULL). offsets NULL: all rows; otherwise
+// (part [dz_strips(rows, N, act)][N], may be NULL). offsets NULL: all rows; otherwise
 // rows [offsets[0], offsets[E]).
-int dz_strips(int rows);
+int dz_strips(int rows, int N, int act);
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
                      int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s);
 // out[n] = sum over parts, in order; out_type 0 bf16, 1 fp16, 2 float32

@@ -238,7 +238,7 @@ constexpr int kMMGroupM = 8;                   // m tiles walked together over a
 
 // Tile of a row-grouped product (NT, NN). Tiles are ordered expert by expert;
 // inside an expert, groups of kMMGroupM m tiles walk the n tiles together. Each
-// XCD (blockIdx % 8) takes a contiguous run of that order, so that the tiles
+// XCD (block % 8) takes a contiguous run of that order, so that the tiles
 // it holds at one time share W strips and x rows in its L2. Offsets are clamped
 // to [0, rows] and a block's end to its start, so that values outside the
 // contract cannot lead out of the buffers. Returns false for a block without a tile.
@@ -251,14 +251,14 @@ __device__ __forceinline__ i32x2_t tr_read(const lds_s16x4_t* __restrict__ p) {
 
 template <int BM, int NTHR>
 __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, int rows, int E,
-                                             int NT, int* sm, MMTile& t) {
+                                             int NT, int* sm, uint32_t bid, MMTile& t) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid >> 6;
   int e = 0, local = 0, mtiles = 0, beg = 0, end = 0;
   if (offsets == nullptr) {
     mtiles = (rows + BM - 1) / BM;
     const int total = mtiles * NT, chunk = (total + 7) / 8;
-    local = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-    if (static_cast<int>(blockIdx.x >> 3) >= chunk || local >= total) return false;
+    local = (bid & 7) * chunk + (bid >> 3);
+    if (static_cast<int>(bid >> 3) >= chunk || local >= total) return false;
     end = rows;
   } else {
     constexpr int kPer = 1024 / NTHR > 0 ? 1024 / NTHR : 1;   // E <= 1024
@@ -294,8 +294,8 @@ __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, in
       total += s;
     }
     const int chunk = (total + 7) / 8;
-    const int tau = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-    if (static_cast<int>(blockIdx.x >> 3) >= chunk || tau >= total) return false;   // uniform
+    const int tau = (bid & 7) * chunk + (bid >> 3);
+    if (static_cast<int>(bid >> 3) >= chunk || tau >= total) return false;   // uniform
     int start = before + incl - sum;
     int* out = sm + NTHR / kWave;
 #pragma unroll
@@ -324,9 +324,11 @@ __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, in
   return true;
 }
 
+// One tile: block `bid` of a grid of its mode's tiles.
 template <class T, int MODE, class G>
-__global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
-    const uint8_t* __restrict__ Ab, const uint8_t* __restrict__ Bb, const MMArgs a) {
+__device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
+                                        const uint8_t* __restrict__ Bb, const MMArgs& a,
+                                        uint32_t bid) {
   constexpr int BM = G::BM, BN = G::BN, BK = G::BK, NTHR = G::kThreads, STAGES = G::STAGES;
   constexpr int MI = G::MI, NJ = G::NJ, CPR = BK / 8, KS = BK / 16;
   constexpr int RW = BM / G::WM, CW = BN / G::WN;   // tile rows / columns per wave
@@ -353,7 +355,7 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
       // slices of m by 8 / xm of n), so that experts with many rows load all XCDs
       // alike (runs of whole experts per XCD: 394 us for 32768 rows, 8 to 1513
       // per expert, against 314 us with 256 each)
-      const int xcd = blockIdx.x & 7, l0 = blockIdx.x >> 3;
+      const int xcd = bid & 7, l0 = bid >> 3;
       const int xn = 8 / a.xm, tm = (a.mt + a.xm - 1) / a.xm, tn = (a.nt + xn - 1) / xn;
       es = l0 / (tm * tn);
       const int l = l0 - es * tm * tn;
@@ -362,8 +364,8 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
       if (es >= a.E * a.splits || mi >= a.mt || ni >= a.nt) return;
     } else {
       const int total = a.E * a.splits * a.mt * a.nt, chunk = (total + 7) / 8;
-      int tau = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-      if (static_cast<int>(blockIdx.x >> 3) >= chunk || tau >= total) return;
+      int tau = (bid & 7) * chunk + (bid >> 3);
+      if (static_cast<int>(bid >> 3) >= chunk || tau >= total) return;
       const int per_e = a.mt * a.nt;
       es = tau / per_e;
       tau -= es * per_e;
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
     k_end = __builtin_amdgcn_readfirstlane(min(k_begin + part, hi));
   } else {
     MMTile t;
-    if (!mm_find_tile<BM, NTHR>(a.offsets, a.rows, a.E, a.nt, sm_tile, t)) return;
+    if (!mm_find_tile<BM, NTHR>(a.offsets, a.rows, a.E, a.nt, sm_tile, bid, t)) return;
     e = t.e;
     m0 = t.p0;
     mrows = t.p1 - t.p0;
@@ -725,6 +727,12 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
+}
+
+template <class T, int MODE, class G>
+__global__ __launch_bounds__(G::kThreads, G::WPE) void mm_kernel(
+    const uint8_t* __restrict__ Ab, const uint8_t* __restrict__ Bb, const MMArgs a) {
+  mm_tile<T, MODE, G>(Ab, Bb, a, blockIdx.x);
 }
 
 }  // namespace moe

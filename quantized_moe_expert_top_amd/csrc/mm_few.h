@@ -31,7 +31,7 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
   __shared__ __attribute__((aligned(16))) float part[WAVES][BM][16];
   __shared__ int sm_tile[NTHR / kWave + 4];
   MMTile t;
-  if (!mm_find_tile<BM, NTHR>(a.offsets, a.rows, a.E, a.nt, sm_tile, t)) return;
+  if (!mm_find_tile<BM, NTHR>(a.offsets, a.rows, a.E, a.nt, sm_tile, blockIdx.x, t)) return;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, kg = lane >> 4;

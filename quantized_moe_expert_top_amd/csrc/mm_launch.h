@@ -53,18 +53,18 @@ inline double mm_cost(const MMCost& c, double tiles, double stages) {
 }
 // The cheapest geometry for row-grouped products (NT, NN): 0 Big, 1 Mid, 2 Wide,
 // 3 Small.
-inline int mm_pick_rows(int rows, int E, int ndim, int kdim) {
+struct MMPick {
+  int geom;
+  double cost;   // us
+};
+inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim) {
   const MMCost* const table[4] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost};
-  int best = 0;
-  double at = 1e300;
+  MMPick best = {0, 1e300};
   for (int i = 0; i < 4; ++i) {
     const MMCost& c = *table[i];
     const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * ((ndim + c.bn - 1) / c.bn),
                                 (kdim + 63) / 64);
-    if (cost < at) {
-      at = cost;
-      best = i;
-    }
+    if (cost < best.cost) best = {i, cost};
   }
   return best;
 }
@@ -75,8 +75,9 @@ inline void mm_set_stream(MMArgs& a, long long values) {
   a.stream_out = bytes > (32LL << 20);
 }
 
-template <class T, int MODE, class G>
-hipError_t mm_launch(MMArgs a, hipStream_t s) {
+// Fills in what the kernel needs of the geometry; returns the grid (a multiple of 8).
+template <int MODE, class G>
+long long mm_prepare(MMArgs& a) {
   long long tiles;
   const bool swiglu = MODE == kModeNT && a.act == kActSwiglu;
   a.nt = swiglu ? (a.ndim / 2 + G::BN / 2 - 1) / (G::BN / 2) : (a.ndim + G::BN - 1) / G::BN;
@@ -105,21 +106,35 @@ hipError_t mm_launch(MMArgs a, hipStream_t s) {
     const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
     tiles = (a.rows / G::BM + partial) * a.nt;
   }
-  const long long grid = (tiles + 7) / 8 * 8;
+  return (tiles + 7) / 8 * 8;
+}
+
+// Dynamic LDS of a kernel: the attribute is set once per device (threads that
+// race set it twice).
+struct MMReady {
+  std::atomic<bool> device[moe_api::kMaxDevices];
+  hipError_t set(const void* kernel, int lds) {
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    if (dev < 0 || dev >= moe_api::kMaxDevices) return hipErrorInvalidDevice;
+    if (!device[dev].load(std::memory_order_acquire)) {
+      e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+      device[dev].store(true, std::memory_order_release);
+    }
+    return hipSuccess;
+  }
+};
+
+template <class T, int MODE, class G>
+hipError_t mm_launch(MMArgs a, hipStream_t s) {
+  const long long grid = mm_prepare<MODE, G>(a);
   if (grid == 0) return hipSuccess;
   if (grid >= (1LL << 31)) return hipErrorInvalidConfiguration;
-  // the attribute is set once per device (threads that race set it twice)
-  static std::atomic<bool> ready[moe_api::kMaxDevices];
-  int dev = -1;
-  hipError_t e = hipGetDevice(&dev);
+  static MMReady ready;
+  const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_kernel<T, MODE, G>), G::kLds);
   if (e != hipSuccess) return e;
-  if (dev < 0 || dev >= moe_api::kMaxDevices) return hipErrorInvalidDevice;
-  if (!ready[dev].load(std::memory_order_acquire)) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&mm_kernel<T, MODE, G>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
-    if (e != hipSuccess) return e;
-    ready[dev].store(true, std::memory_order_release);
-  }
   hipLaunchKernelGGL((mm_kernel<T, MODE, G>), dim3(static_cast<unsigned>(grid)),
                      dim3(G::kThreads), G::kLds, s,
                      static_cast<const uint8_t*>(a.A), static_cast<const uint8_t*>(a.B), a);

@@ -7,7 +7,7 @@ namespace {
 
 template <class T>
 hipError_t launch(const MMArgs& a, hipStream_t s) {
-  switch (mm_pick_rows(a.rows, a.offsets ? a.E : 0, a.ndim, a.kdim)) {
+  switch (mm_pick_rows(a.rows, a.offsets ? a.E : 0, a.ndim, a.kdim).geom) {
     case 0: return mm_launch<T, kModeNN, MMBig>(a, s);
     case 1: return mm_launch<T, kModeNN, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNN, MMWide>(a, s);

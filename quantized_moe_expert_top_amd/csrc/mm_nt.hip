@@ -20,7 +20,7 @@ hipError_t launch(const MMArgs& a, hipStream_t s) {
     if (E != 0 || a.rows <= 16) return mm_few_launch<T, 1, 8, 2>(a, s);
     return mm_few_launch<T, 2, 8, 2>(a, s);
   }
-  switch (mm_pick_rows(a.rows, E, a.ndim, a.kdim)) {
+  switch (mm_pick_rows(a.rows, E, a.ndim, a.kdim).geom) {
     case 0: return mm_launch<T, kModeNT, MMBig>(a, s);
     case 1: return mm_launch<T, kModeNT, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNT, MMWide>(a, s);
