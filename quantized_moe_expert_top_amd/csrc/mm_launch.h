@@ -11,6 +11,12 @@ using MMBig = MMGeom<256, 256, 4, 2, 64, 2, 2>;    // 8 waves, one block per CU
 using MMMid = MMGeom<128, 128, 2, 2, 64, 2, 2>;    // 4 waves, two blocks per CU
 using MMWide = MMGeom<64, 128, 2, 4, 64, 3, 4>;    // 8 waves, two blocks per CU
 using MMSmall = MMGeom<64, 64, 2, 2, 64, 4, 2>;    // 4 waves, two blocks per CU
+// 4 waves, two blocks per CU: one block's loads and epilogue stand behind the
+// other's multiplies. Its 32-k stages read half cache lines of a K-major operand,
+// so a long K goes to Big (8192 x 4096 x 7168: 447 us expected against 376); with
+// few stages it wins (128 experts, 32768 rows x 2048 x 768 to float32: 215 against
+// 240 us; its row gradient 150 against 167).
+using MMLong = MMGeom<128, 256, 2, 2, 32, 3, 2>;
 
 // What a geometry costs, in us on one MI355X: a round of resident blocks takes
 // `s1`, `s2` or `s3` per 64-k stage with 64, 256 or `slots` blocks at work (fewer
@@ -31,6 +37,7 @@ constexpr MMCost kMMBigCost = {256, 256, 256, 1.12, 1.64, 1.64, 9.0, 9.0};
 constexpr MMCost kMMMidCost = {128, 128, 512, 0.57, 0.65, 0.96, 9.0, 4.0};
 constexpr MMCost kMMWideCost = {64, 128, 512, 0.30, 0.36, 0.65, 6.5, 3.8};
 constexpr MMCost kMMSmallCost = {64, 64, 512, 0.20, 0.23, 0.40, 5.0, 3.5};
+constexpr MMCost kMMLongCost = {128, 256, 512, 1.00, 1.20, 1.90, 11.0, 5.0};
 
 // m tiles of row blocks: of `rows` rows in one block (E = 0), or spread over E
 // experts, where about half a tile per expert in use is left over and none has
@@ -52,16 +59,21 @@ inline double mm_cost(const MMCost& c, double tiles, double stages) {
   return cost;
 }
 // The cheapest geometry for row-grouped products (NT, NN): 0 Big, 1 Mid, 2 Wide,
-// 3 Small.
+// 3 Small, 4 Long. Experts of few rows are bound by streaming their weights, which
+// the low tiles keep most loads in flight for (128 experts x 1536 x 2048: 8192 rows
+// Wide 181, Long 207, Mid 216, Big 249 us; 4096 rows 166, -, 189, 200).
 struct MMPick {
   int geom;
   double cost;   // us
 };
 inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim) {
-  const MMCost* const table[4] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost};
+  const MMCost* const table[5] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost,
+                                  &kMMLongCost};
+  const bool low = E > 1 && rows <= 96LL * (rows < E ? rows : E);
   MMPick best = {0, 1e300};
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 5; ++i) {
     const MMCost& c = *table[i];
+    if (low && c.bm > 64) continue;
     const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * ((ndim + c.bn - 1) / c.bn),
                                 (kdim + 63) / 64);
     if (cost < best.cost) best = {i, cost};

@@ -11,7 +11,8 @@ hipError_t launch(const MMArgs& a, hipStream_t s) {
     case 0: return mm_launch<T, kModeNN, MMBig>(a, s);
     case 1: return mm_launch<T, kModeNN, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNN, MMWide>(a, s);
-    default: return mm_launch<T, kModeNN, MMSmall>(a, s);
+    case 3: return mm_launch<T, kModeNN, MMSmall>(a, s);
+    default: return mm_launch<T, kModeNN, MMLong>(a, s);
   }
 }
 

@@ -24,7 +24,8 @@ hipError_t launch(const MMArgs& a, hipStream_t s) {
     case 0: return mm_launch<T, kModeNT, MMBig>(a, s);
     case 1: return mm_launch<T, kModeNT, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNT, MMWide>(a, s);
-    default: return mm_launch<T, kModeNT, MMSmall>(a, s);
+    case 3: return mm_launch<T, kModeNT, MMSmall>(a, s);
+    default: return mm_launch<T, kModeNT, MMLong>(a, s);
   }
 }
 

@@ -820,3 +820,96 @@ def test_block_forward_and_backward_together():
         g, v = got.double().cpu(), want.detach()
         rel = ((g - v).norm() / v.norm()).item()
         assert rel <= tol, f"{name}: relative 2-norm {rel:.3g} > {tol:.3g}"
+
+
+# ------------------------------------------------------- every tile geometry --
+# Shapes that reach each geometry of the products (256x256, 128x256 and 256x128
+# with 32-deep stages, 128x128, 64x128, 64x64, the split contraction and both
+# gradients in one launch), with odd remainders in every direction.
+GEOMETRIES = [
+    # rows, K, N, experts (0: dense)
+    (8200, 4104, 7184, 0), (2500, 264, 4112, 0), (4093, 2048, 1536, 0), (1100, 96, 2048, 0),
+    (40000, 72, 80, 0), (700, 2056, 1040, 0), (8200, 4104, 7184, 3), (4000, 2056, 1040, 6),
+    (9000, 1032, 2064, 3), (300, 64, 2064, 40), (12000, 520, 2064, 3), (16000, 1032, 2064, 60),
+]
+
+
+def _splits(rows, E, seed):
+    g = torch.Generator().manual_seed(seed)
+    w = torch.rand(E, generator=g) ** 2 + 0.02
+    n = (w / w.sum() * rows).long()
+    n[E // 2] = 0
+    n[0] += rows - 7 - int(n.sum())      # the last 7 rows belong to no expert
+    return _offsets(n.tolist())
+
+
+@pytest.mark.parametrize("rows,K,N,E", GEOMETRIES)
+def test_every_geometry(rows, K, N, E):
+    import quantized_moe_expert_top_amd as moe
+    i = GEOMETRIES.index((rows, K, N, E))
+    t = (BF, HF)[i % 2]
+    act = ("swiglu", "none")[i % 2]
+    _say("geometry", rows, K, N, E, t, act)
+    mk = Maker(300 + i)
+    No = N // 2 if act == "swiglu" else N
+    off = _splits(rows, E, i) if E else [0, rows]
+    oft = torch.tensor(off, dtype=torch.int32, device="cuda")
+    gather, topk = E > 0 and i % 3 != 1, 4
+    slot, src, tokens = _sources(i, rows, gather, topk)
+    x, dy = mk((tokens, K), t), mk((rows, No), t)
+    w = mk((max(E, 1), N, K), t, K ** -0.5)
+    y, ycheck = guarded((rows, No), t)
+    z, zcheck = guarded((rows, N), t)
+    bias = mk((N,), t) if not E else None
+    res = mk((rows, No), t) if not E else None
+    if E:
+        moe.grouped_mm(x, w, oft, y, sorted_slot=slot, topk=topk, act=act, z=z)
+    else:
+        moe.linear(x, w[0], y, bias=bias, residual=res, act=act, z=z)
+    torch.cuda.synchronize()
+    xs = x[src]
+    zz = mk((rows, N), t) if act != "none" else None
+    n_ws = (moe.grouped_mm_backward_workspace(rows, K, N, E, act) if E else
+            moe.linear_backward_workspace(rows, K, N, act))
+    ws = workspace(n_ws)
+
+    def grads(dx, dw):
+        if E:
+            moe.grouped_mm_backward(dy, x, w, oft, dx=dx, dw=dw, sorted_slot=slot, topk=topk,
+                                    act=act, z=zz, ws=ws)
+        else:
+            moe.linear_backward(dy, x, w[0], dx=dx, dw=None if dw is None else dw[0], act=act, z=zz,
+                                ws=ws)
+    both, apart = [], []
+    for outs, calls in ((both, ((1, 1),)), (apart, ((1, 0), (0, 1)))):
+        dx, cx = guarded((rows, K), t)
+        dw, cw = guarded((max(E, 1), N, K), t)
+        for want_dx, want_dw in calls:
+            grads(dx if want_dx else None, dw if want_dw else None)
+        torch.cuda.synchronize()
+        cx("dx")
+        cw("dw")
+        outs.extend((dx, dw))
+    for e in range(max(E, 1)):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            assert (both[1][e] == 0).all() and (apart[1][e] == 0).all()
+            continue
+        xd, wd = xs[a:b].double(), w[e].double()
+        zr, ez = ref.product(xd, wd, None if bias is None else bias.double())
+        yr, by = ref.epilogue(zr, ez, act, None if res is None else res.double(), t)
+        close(z[a:b], zr, rounded(zr, ez, t), f"z of expert {e}")
+        close(y[a:b], yr, by, f"y of expert {e}")
+        del zr, ez, yr, by
+        dz, edz, _ = ref.dz_pair(dy[a:b].double(), zz[a:b].double() if zz is not None else None, act, t)
+        rdx, mdx = dz @ wd, (dz.abs() + edz) @ wd.abs()
+        bdx = rounded(rdx, edz @ wd.abs() + (N + 2) * ref.F * mdx, t)
+        rdw, mdw = dz.t() @ xd, (dz.abs() + edz).t() @ xd.abs()
+        bdw = rounded(rdw, edz.t() @ xd.abs() + (b - a + 2) * ref.F * mdw, t)
+        for dx, dw in (both, apart):
+            close(dx[a:b], rdx, bdx, f"dx of expert {e}")
+            close(dw[e], rdw, bdw, f"dw of expert {e}")
+    ycheck("y")
+    zcheck("z")
+    for o in (y, z, both[0], apart[0]):
+        assert torch.isnan(o[off[-1]:]).all()
