@@ -18,6 +18,7 @@ using moe_api::launched;
 
 constexpr int64_t kMaxFeatures = 1 << 20;    // K and N: 32-bit offsets inside a tile's rows
 constexpr int64_t kMaxResource = 1LL << 30;  // values behind one buffer resource (2 GiB)
+constexpr int32_t kMaxRows = INT32_MAX - 65535;   // room for the ends of tiles and splits
 constexpr int64_t kMaxValues = 1LL << 38;    // values of one array: bounds every grid
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -27,6 +28,7 @@ int out_width(const moe_mm_shape* s) { return s->act == MOE_ACT_SWIGLU ? s->N / 
 moe_status check_mm(const moe_mm_shape* s, bool grouped) {
   if (!s) return fail(MOE_EINVAL, "shape is NULL");
   if (s->rows < 0) return fail(MOE_EINVAL, "rows = %d < 0", s->rows);
+  if (s->rows > kMaxRows) return fail(MOE_ESHAPE, "rows = %d above %d", s->rows, kMaxRows);
   if (s->dtype != MOE_BF16 && s->dtype != MOE_FP16)
     return fail(MOE_EINVAL, "dtype = %d is neither MOE_BF16 nor MOE_FP16", s->dtype);
   if (s->act < MOE_ACT_NONE || s->act > MOE_ACT_SWIGLU)
@@ -244,7 +246,7 @@ moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy, co
                            {"dw", dw, shape->E * values(shape->N, shape->K, dw_dtype), true},
                            {"ws", ws, need.total, true},
                            {"dy", dy, values(rows, out_width(shape), t), false},
-                           {"x", x, values(sorted_slot ? shape->x_rows : rows, shape->K, t), false},
+                           {"x", dw ? x : nullptr, values(sorted_slot ? shape->x_rows : rows, shape->K, t), false},
                            {"w", w, shape->E * values(shape->N, shape->K, t), false},
                            {"z", z, values(rows, shape->N, t), false},
                            {"expert_offsets", expert_offsets, (shape->E + 1) * size_t{4}, false},

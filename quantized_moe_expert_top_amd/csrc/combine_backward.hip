@@ -37,7 +37,7 @@ __device__ __forceinline__ void store_dy(void* dy, size_t at, const float (&v)[8
 template <int DY, bool STREAM>
 __global__ __launch_bounds__(512) void combine_backward_kernel(
     const float* __restrict__ dout, const float* __restrict__ y, const int* __restrict__ slot_pos,
-    const int* __restrict__ ids, const float* __restrict__ w, int T, int H, int E, int k,
+    const int* __restrict__ ids, const float* __restrict__ w, long long R, int H, int E, int k,
     void* __restrict__ dy, float* __restrict__ dw, float* __restrict__ dlogits) {
   __shared__ float sdw[kMaxPicks];
   __shared__ float swt[kMaxPicks];
@@ -45,7 +45,6 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(
   const int t = blockIdx.x, lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
   const int waves = blockDim.x >> 6;
   const int C = H / 8;
-  const long long R = static_cast<long long>(T) * k;
   const float* drow = dout + static_cast<size_t>(t) * H;
   const bool need_dot = dw != nullptr || dlogits != nullptr;
   for (int j = wv; j < k; j += waves) {
@@ -100,11 +99,19 @@ hipError_t launch_combine_backward(const float* dout, const float* y, const int*
                                    hipStream_t s) {
   if (T == 0) return hipSuccess;
   const int threads = k > 4 ? 512 : k > 2 ? 256 : k > 1 ? 128 : 64;
-  const bool stream = dy && static_cast<long long>(T) * k * H * (dy_type == 2 ? 4 : 2) > (32LL << 20);
+  const long long R = static_cast<long long>(T) * k;
+  const bool stream = dy && R * H * (dy_type == 2 ? 4 : 2) > (32LL << 20);
   auto launch = [&](auto dyc) {
     constexpr int DY = decltype(dyc)::value;
-    if (stream) combine_backward_kernel<DY, true><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
-    else combine_backward_kernel<DY, false><<<T, threads, 0, s>>>(dout, y, slot_pos, ids, w, T, H, E, k, dy, dw, dlogits);
+    // one launch holds less than 2^32 threads: 2^22 tokens of 512
+    constexpr int kLaunchTokens = 1 << 22;
+    for (long long t0 = 0; t0 < T; t0 += kLaunchTokens) {
+      const unsigned n = static_cast<unsigned>(T - t0 < kLaunchTokens ? T - t0 : kLaunchTokens);
+      const auto run = stream ? &combine_backward_kernel<DY, true> : &combine_backward_kernel<DY, false>;
+      run<<<n, threads, 0, s>>>(dout + t0 * H, y, slot_pos + t0 * k, ids ? ids + t0 * k : nullptr,
+                                w + t0 * k, R, H, E, k, dy, dw ? dw + t0 * k : nullptr,
+                                dlogits ? dlogits + t0 * E : nullptr);
+    }
   };
   if (dy_type == 0) launch(std::integral_constant<int, 0>{});
   else if (dy_type == 1) launch(std::integral_constant<int, 1>{});

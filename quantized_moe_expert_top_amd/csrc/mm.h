@@ -233,6 +233,12 @@ __device__ __forceinline__ void mm_interleave() {
 }
 
 constexpr uint32_t kMMPastEnd = 0x80000000u;   // at or past the end of every resource here
+
+// Whether a launch fits: under 2^32 threads, and under 2^31 tiles whatever the
+// offsets hold (each of E experts all the rows).
+inline bool mm_fits(long long grid, int threads, long long expert_tiles, int E) {
+  return grid * threads < (1LL << 32) && expert_tiles * E < (1LL << 31);
+}
 constexpr int kMMSegRows = 1024;               // TN gather: source rows held in LDS at a time
 constexpr int kMMGroupM = 8;                   // m tiles walked together over all n tiles
 

@@ -148,7 +148,8 @@ hipError_t mm_few_launch(MMArgs a, hipStream_t s) {
   const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
   const long long grid = ((a.rows / (16 * MT) + partial) * a.nt + 7) / 8 * 8;
   if (grid == 0) return hipSuccess;
-  if (grid >= (1LL << 31)) return hipErrorInvalidConfiguration;
+  if (!mm_fits(grid, WAVES * 64, (a.rows / (16 * MT) + 1LL) * a.nt, a.E))
+    return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((mm_few_kernel<T, MT, WAVES, U>), dim3(static_cast<unsigned>(grid)),
                      dim3(WAVES * 64), 0, s, static_cast<const uint8_t*>(a.A),
                      static_cast<const uint8_t*>(a.B), a);

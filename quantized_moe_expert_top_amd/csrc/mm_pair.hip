@@ -19,7 +19,8 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_pair_kernel(
 template <class T, class G>
 hipError_t launch(MMArgs nn, MMArgs tn, hipStream_t s) {
   const long long tb = mm_prepare<kModeTN, G>(tn), nb = mm_prepare<kModeNN, G>(nn);
-  if (tb + nb >= (1LL << 31)) return hipErrorInvalidConfiguration;
+  if (!mm_fits(tb + nb, G::kThreads, (nn.rows / G::BM + 1LL) * nn.nt, nn.E))
+    return hipErrorInvalidConfiguration;
   static MMReady ready;
   const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_pair_kernel<T, G>), G::kLds);
   if (e != hipSuccess) return e;

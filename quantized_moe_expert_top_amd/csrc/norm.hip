@@ -331,7 +331,7 @@ __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(const NormA
     block_sum3<W>(s1, s2, s3, red[0]);
     const float q = 1.0f / sqrtf(s1 * inv_h + a.eps);
     const float p = a.w_post ? 1.0f / sqrtf(s3 * inv_h + a.eps) : 1.0f;
-    const float back = q * q * q * s2 * inv_h;
+    const float back = s2 * inv_h * q * q * q;   // 0 for a row of zeros at any eps
     const float tg = a.gate_kind == 2 ? load1<T>(a.gate, t) : 1.0f;
     float s4 = 0.0f, s5 = 0.0f, s6 = 0.0f;
 #pragma unroll kUnroll
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(const NormA
     }
     if (a.y) {
       block_sum3<W>(s4, s5, s6, red[1]);
-      const float bk = a.w_post ? p * p * p * s4 * inv_h : 0.0f;
+      const float bk = a.w_post ? s4 * inv_h * p * p * p : 0.0f;
       if (a.dy)
 #pragma unroll kUnroll
         for (int i = 0; i < NC; ++i) {
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(kNormWaves * 64, NC == 1 ? 4 : 2) void block_norm_b
     s3 = wave_sum_f32(s3);
     const float q = 1.0f / sqrtf(s1 * inv_h + a.eps);
     const float p = a.w_post ? 1.0f / sqrtf(s3 * inv_h + a.eps) : 1.0f;
-    const float back = q * q * q * s2 * inv_h;
+    const float back = s2 * inv_h * q * q * q;   // 0 for a row of zeros at any eps
     const float tg = a.gate_kind == 2 ? load1<T>(a.gate, t) : 1.0f;
     float s4 = 0.0f, s5 = 0.0f;
 #pragma unroll
@@ -516,7 +516,7 @@ __global__ __launch_bounds__(kNormWaves * 64, NC == 1 ? 4 : 2) void block_norm_b
     if (a.y) {
       s4 = wave_sum_f32(s4);
       s5 = wave_sum_f32(s5);
-      const float bk = a.w_post ? p * p * p * s4 * inv_h : 0.0f;
+      const float bk = a.w_post ? s4 * inv_h * p * p * p : 0.0f;
       if (a.dy)
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -610,6 +610,22 @@ hipError_t backward(const NormArgs& a, int blocks, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The forward's operands from row t0 on.
+NormArgs rows_from(NormArgs a, int t0, int rows) {
+  const size_t at = static_cast<size_t>(t0) * a.H, rb = a.r_f32 ? 4 : 2, yb = a.y_f32 ? 4 : 2;
+  auto from = [](auto& p, size_t bytes) {
+    using P = typename std::remove_reference<decltype(p)>::type;
+    if (p) p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p) + bytes);
+  };
+  from(a.r, at * rb);
+  from(a.y, at * yb);
+  from(a.r_out, at * rb);
+  from(a.h, at * 2);
+  if (a.gate_kind >= 2) from(a.gate, (a.gate_kind == 3 ? at : static_cast<size_t>(t0)) * 2);
+  a.T = rows;
+  return a;
+}
+
 bool streams(const NormArgs& a, long long bytes_per_value) {
   return static_cast<long long>(a.T) * a.H * bytes_per_value > (32LL << 20);
 }
@@ -617,10 +633,17 @@ bool streams(const NormArgs& a, long long bytes_per_value) {
 }  // namespace
 
 hipError_t launch_block_norm(const NormArgs& a, bool fp16, hipStream_t s) {
-  if (a.T == 0) return hipSuccess;
-  if (streams(a, (a.r_out ? (a.r_f32 ? 4 : 2) : 0) + (a.h ? 2 : 0)))
-    return fp16 ? forward<fp16_tag, true>(a, s) : forward<bf16_tag, true>(a, s);
-  return fp16 ? forward<fp16_tag, false>(a, s) : forward<bf16_tag, false>(a, s);
+  const bool stream = streams(a, (a.r_out ? (a.r_f32 ? 4 : 2) : 0) + (a.h ? 2 : 0));
+  // one launch holds less than 2^32 threads: 2^21 rows of 1024
+  constexpr int kLaunchRows = 1 << 21;
+  for (int t0 = 0, left = a.T; left > 0; left -= kLaunchRows, t0 += kLaunchRows) {
+    const NormArgs p = rows_from(a, t0, left < kLaunchRows ? left : kLaunchRows);
+    const hipError_t e = stream ? (fp16 ? forward<fp16_tag, true>(p, s) : forward<bf16_tag, true>(p, s))
+                                : (fp16 ? forward<fp16_tag, false>(p, s) : forward<bf16_tag, false>(p, s));
+    if (e != hipSuccess) return e;
+    if (left <= kLaunchRows) break;
+  }
+  return hipSuccess;
 }
 
 int norm_backward_blocks(int T, int H) {
