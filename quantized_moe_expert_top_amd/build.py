@@ -45,6 +45,9 @@ FLAGS = [
 ]
 
 
+BINDING = os.path.join(HERE, "_block_binding.so")   # CPython module, host code only
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), shutil.which("hipcc"), "/opt/rocm/bin/hipcc"):
         if cand and os.path.exists(cand):
@@ -88,10 +91,31 @@ def _compile(src: str):
     return obj, kernel_resources(r.stderr)
 
 
+def _build_binding() -> str:
+    """The CPython binding of the block operators: g++ against torch's headers."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for p in inc for f in ("-isystem", p)], os.path.join(CSRC, "block_binding.cpp"),
+           "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on block_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        binding = ex.submit(_build_binding)
         done = list(ex.map(_compile, SOURCES))
+        binding.result()
     objs = [o for o, _ in done]
     resources = {k: v for _, res in done for k, v in res.items()}
     if not resources:

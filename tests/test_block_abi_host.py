@@ -54,6 +54,7 @@ BAD_SHAPES = [
     (dict(K=(1 << 20) + 8), ESHAPE), (dict(N=(1 << 20) + 8), ESHAPE),
     (dict(N=1 << 16, K=1 << 15), ESHAPE),                       # N*K = 2^31
     (dict(rows=(1 << 31) - 1, N=1 << 10), ESHAPE),              # rows*N above 2^38
+    (dict(rows=(1 << 31) - 1, K=8, N=16), ESHAPE), (dict(rows=(1 << 31) - 65535, K=8, N=16), ESHAPE),
 ]
 
 
@@ -297,6 +298,34 @@ def test_binding_refuses_shapes_types_and_layouts():
         except ValueError:
             continue
         pytest.fail(f"call {i} was not refused")
+
+
+def test_binding_refuses_what_is_no_tensor():
+    """Missing and foreign operands, numbers that do not fit, tensors without memory."""
+    import quantized_moe_expert_top_amd as moe
+    x, w, y = _t((2, 16)), _t((32, 16)), _t((2, 32))
+    off, w3, slot = torch.zeros(2, dtype=torch.int32), w[None], torch.zeros(2, dtype=torch.int32)
+    for bad in ([1.0], None, "x", 3):
+        with pytest.raises(ValueError):
+            moe.linear(bad, w, y)
+        with pytest.raises(ValueError):
+            moe.block_norm(bad, h=x)
+    with pytest.raises(ValueError):
+        moe.linear(x, w, None)
+    with pytest.raises(ValueError):
+        moe.linear(x.to("meta"), w.to("meta"), y.to("meta"))
+    with pytest.raises(ValueError):
+        moe.linear(x, w, y, residual=y.to("meta"))
+    with pytest.raises(ValueError):
+        moe.linear(x, w, y, act="tanh")
+    with pytest.raises(ValueError):
+        moe.grouped_mm(x, w3, off, y, sorted_slot=slot, topk=1 << 40)
+    with pytest.raises(TypeError):
+        moe.grouped_mm(x, w3, off, y, sorted_slot=slot, topk=1.5)
+    with pytest.raises(TypeError):
+        moe.block_norm(x, h=x, w_pre=w[0], eps="small")
+    with pytest.raises(TypeError):
+        moe.block_norm(x, h=x, w_pre=w[0], bias=w[0])
 
 
 def test_overlaps_refused():

@@ -664,6 +664,47 @@ def test_two_streams_at_once():
     _same(bout, wb, "current stream")
 
 
+def test_two_threads_at_once():
+    import threading
+    sets = [_block_calls(i) for i in (1, 2)]
+    for calls, _ in sets:
+        calls()
+    torch.cuda.synchronize()
+    wants = [[o.clone() for o in outs] for _, outs in sets]
+    for _, outs in sets:
+        for o in outs:
+            o.fill_(float("nan"))
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(calls):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    calls()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(calls,)) for calls, _ in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for (_, outs), want in zip(sets, wants):
+        _same(outs, want, "two threads")
+
+
+def test_host_tensors_are_refused():
+    import quantized_moe_expert_top_amd as moe
+    x, w = torch.zeros((2, 16), dtype=BF), torch.zeros((32, 16), dtype=BF)
+    with pytest.raises(ValueError):
+        moe.linear(x, w, torch.zeros((2, 32), dtype=BF))
+    with pytest.raises(ValueError):
+        moe.linear(x.cuda(), w, torch.zeros((2, 32), dtype=BF, device="cuda"))
+
+
 def test_two_graphs_replayed_with_eager_work_between():
     a, aout = _block_calls(1)
     b, bout = _block_calls(2)
