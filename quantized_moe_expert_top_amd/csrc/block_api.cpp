@@ -122,10 +122,11 @@ MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   return w;
 }
 
-// dx = dz W, dw = dz^T x on the given dz
+// dx = dz W, dw = dz^T x on the given dz, and `sum` (may be empty)
 moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* x, const void* w,
                              const int32_t* offsets, const int32_t* slot, void* dx, int dx_dtype,
-                             void* dw, int dw_dtype, void* parts, hipStream_t st) {
+                             void* dw, int dw_dtype, void* parts, const moe::PartSum& sum,
+                             hipStream_t st) {
   const bool fp16 = s->dtype == MOE_FP16;
   moe::MMArgs nn = mm_args(s, offsets, nullptr);
   nn.A = dz;
@@ -143,7 +144,11 @@ moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* 
   tn.c_f32 = dw_dtype == MOE_F32;
   if (dx && dw && s->rows > 0) {
     const int pick = moe::mm_pair_pick(s->rows, offsets ? s->E : 0, s->N, s->K);
-    if (pick) return launched(moe::launch_mm_pair(nn, tn, pick, fp16, st), "gradient launch");
+    if (pick) return launched(moe::launch_mm_pair(nn, tn, sum, pick, fp16, st), "gradient launch");
+  }
+  if (sum.out) {
+    const moe_status r = launched(moe::launch_sum_parts(sum, st), "bias gradient launch");
+    if (r) return r;
   }
   if (dx && s->rows > 0) {
     const moe_status r = launched(moe::launch_mm_nn(nn, fp16, st), "row gradient launch");
@@ -265,7 +270,7 @@ moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy, co
     dz = out;
   }
   return products_backward(shape, dz, x, w, expert_offsets, shape->rows > 0 ? sorted_slot : nullptr,
-                           dx, dx_dtype, dw, dw_dtype, base + need.parts, s);
+                           dx, dx_dtype, dw, dw_dtype, base + need.parts, {}, s);
 }
 
 moe_status moe_linear(const moe_mm_shape* shape, const void* x, const void* w, const void* bias,
@@ -362,15 +367,10 @@ moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_
                   "activation gradient launch");
     if (st) return st;
   }
-  if (dbias) {
-    st = launched(moe::launch_sum_parts(strips, moe::dz_strips(shape->rows, shape->N, shape->act), shape->N, dbias,
-                                        dw_dtype, s),
-                  "bias gradient launch");
-    if (st) return st;
-  }
-  if (!dx && !dw) return MOE_OK;
+  const moe::PartSum sum = {strips, dbias ? moe::dz_strips(shape->rows, shape->N, shape->act) : 0,
+                            shape->N, dbias, dw_dtype};
   return products_backward(shape, dz, x, w, nullptr, nullptr, dx, dx_dtype, dw, dw_dtype,
-                           base + need.parts, s);
+                           base + need.parts, sum, s);
 }
 
 static moe_status check_norm(const moe_norm_shape* s) {

@@ -2,6 +2,7 @@
 // partial sums, and sums of float32 parts.
 #include "launch_block.h"
 #include "mm.h"
+#include "part_sum.h"
 
 namespace moe {
 namespace {
@@ -160,30 +161,8 @@ __global__ __launch_bounds__(256) void dz_flat_kernel(const void* __restrict__ d
   }
 }
 
-__device__ __forceinline__ void store_as(void* out, long long i, float v, int type) {
-  if (type == 2) static_cast<float*>(out)[i] = v;
-  else if (type == 0) static_cast<uint16_t*>(out)[i] = f32_to_bf16(v);
-  else static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(pack2<fp16_tag>(v, 0.0f));
-}
-
-// 32 columns x 8 runs of parts per block; the runs are joined in order.
-__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ part, int parts,
-                                                        long long n, void* __restrict__ out,
-                                                        int type) {
-  __shared__ float red[8][32];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const long long col = static_cast<long long>(blockIdx.x) * 32 + tx;
-  const int run = (parts + 7) / 8, p0 = ty * run, p1 = min(p0 + run, parts);
-  float v = 0.0f;
-  if (col < n)
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) v += part[static_cast<size_t>(p) * n + col];
-  red[ty][tx] = v;
-  __syncthreads();
-  if (ty == 0 && col < n) {
-    for (int y = 1; y < 8; ++y) v += red[y][tx];
-    store_as(out, col, v, type);
-  }
+__global__ __launch_bounds__(256) void sum_parts_kernel(const PartSum a) {
+  sum_parts_block(a, blockIdx.x);
 }
 
 __global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part,
@@ -258,10 +237,8 @@ hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offs
   return hipGetLastError();
 }
 
-hipError_t launch_sum_parts(const float* part, int parts, long long n, void* out, int out_type,
-                            hipStream_t s) {
-  const unsigned grid = static_cast<unsigned>((n + 31) / 32);
-  sum_parts_kernel<<<grid, 256, 0, s>>>(part, parts, n, out, out_type);
+hipError_t launch_sum_parts(const PartSum& sum, hipStream_t s) {
+  sum_parts_kernel<<<sum_parts_blocks(sum), 256, 0, s>>>(sum);
   return hipGetLastError();
 }
 

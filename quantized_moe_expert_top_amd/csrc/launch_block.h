@@ -11,9 +11,19 @@ struct MMArgs;
 hipError_t launch_mm_nt(const MMArgs& a, bool fp16, hipStream_t s);
 hipError_t launch_mm_nn(const MMArgs& a, bool fp16, hipStream_t s);
 hipError_t launch_mm_tn(const MMArgs& a, bool fp16, hipStream_t s);
-// Both gradients in one launch; pick from mm_pair_pick (E 0: no experts), 0 = apart.
+// out[n] = sum of part[parts][n] in order; out_type 0 bf16, 1 fp16, 2 float32.
+// out NULL: none.
+struct PartSum {
+  const float* part;
+  int parts, n;
+  void* out;
+  int out_type;
+};
+// Both gradients, and a sum, in one launch; pick from mm_pair_pick (E 0: no
+// experts), 0 = apart.
 int mm_pair_pick(int rows, int E, int N, int K);
-hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, int pick, bool fp16, hipStream_t s);
+hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pick,
+                          bool fp16, hipStream_t s);
 int mm_tn_splits(int rows, int E, int mdim, int ndim);
 
 // dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
@@ -22,9 +32,7 @@ int mm_tn_splits(int rows, int E, int mdim, int ndim);
 int dz_strips(int rows, int N, int act);
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
                      int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s);
-// out[n] = sum over parts, in order; out_type 0 bf16, 1 fp16, 2 float32
-hipError_t launch_sum_parts(const float* part, int parts, long long n, void* out, int out_type,
-                            hipStream_t s);
+hipError_t launch_sum_parts(const PartSum& sum, hipStream_t s);
 // the same per expert: out[e][n] = sum_s part[e][s][n] (n a multiple of 4)
 hipError_t launch_sum_splits(const float* part, int E, int splits, long long n, void* out,
                              int out_type, hipStream_t s);
