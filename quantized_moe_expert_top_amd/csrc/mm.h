@@ -109,8 +109,7 @@ __device__ __forceinline__ void mm_area8(const float* p, float (&v)[8]) {
   }
 }
 template <class T>
-__device__ __forceinline__ void mm_add8(const uint16_t* p, float (&v)[8]) {
-  const uint4 w = ld16(p);
+__device__ __forceinline__ void mm_add8(const uint4& w, float (&v)[8]) {
   const uint32_t d[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
@@ -629,6 +628,45 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
     for (; st < ns; ++st) stage(st, std::false_type{});
   };
 
+  // ---- where the results go
+  const int out_w = swiglu ? half_n : a.ndim;
+  const int wcols = swiglu ? CW / 2 : CW;        // output columns of the wave
+  const size_t crow = static_cast<size_t>(m0) +
+                      (MODE == kModeTN ? (static_cast<size_t>(e) * a.splits + split) * a.mdim : 0);
+  const int col0 = n0 + wn * wcols;
+  const int per_row = wcols / 8;                 // lanes per row
+  // what is added to 8 columns of a row (NT), as it is stored
+  struct Added {
+    uint4 bias, bias_up, res, res_hi;   // bias_up: SwiGLU; res_hi: float32
+  };
+  auto load_added = [&](int row, int col, Added& v) {
+    if (a.bias) {
+      v.bias = ld16(static_cast<const uint16_t*>(a.bias) + col);
+      if (swiglu) v.bias_up = ld16(static_cast<const uint16_t*>(a.bias) + half_n + col);
+    }
+    if (a.residual) {
+      const size_t at = (crow + row) * out_w + col;
+      if (a.c_f32) {
+        v.res = ld16(static_cast<const float*>(a.residual) + at);
+        v.res_hi = ld16(static_cast<const float*>(a.residual) + at + 4);
+      } else {
+        v.res = ld16(static_cast<const uint16_t*>(a.residual) + at);
+      }
+    }
+  };
+  // Waves of one subtile: both of their row pieces are requested here, ahead of the
+  // products.
+  constexpr bool kAhead = MODE == kModeNT && MI * NJ == 1;
+  Added ahead[2];
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int it = lane + x * kWave, r = it / per_row;
+      const int row = wm * RW + r, col = col0 + (it - r * per_row) * 8;
+      if (r < 32 && row < mrows && col < out_w) load_added(row, col, ahead[x]);
+    }
+  }
+
   constexpr int kSegSteps = kMMSegRows / BK;
   const int seg_len = MODE == kModeTN && gather ? kSegSteps : steps;
   for (int seg0 = 0; seg0 < steps; seg0 += seg_len) {
@@ -658,19 +696,13 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
   constexpr int kRowF = CW + 4;   // floats per row of the area; + 4: banks
   float* area = reinterpret_cast<float*>(mm_lds) + wvu * 32 * kRowF;
   const bool stream = a.stream_out != 0;
-  const int out_w = swiglu ? half_n : a.ndim;
-  const int wcols = swiglu ? CW / 2 : CW;        // output columns of the wave
   // rows of C and z: at most 256 of 2^20 values, so 32-bit offsets
-  const size_t crow = static_cast<size_t>(m0) +
-                      (MODE == kModeTN ? (static_cast<size_t>(e) * a.splits + split) * a.mdim : 0);
   const uint32_t cbytes = static_cast<uint32_t>(out_w) * (a.c_f32 ? 4 : 2);
   const __amdgpu_buffer_rsrc_t c_rs =
       buffer_rsrc(static_cast<uint8_t*>(a.C) + crow * cbytes, mrows * cbytes);
   const __amdgpu_buffer_rsrc_t z_rs =
       buffer_rsrc(static_cast<uint8_t*>(a.z) + (MODE == kModeNT && a.z ? crow * nb : 0),
                   MODE == kModeNT && a.z ? mrows * nb : 0);
-  const int col0 = n0 + wn * wcols;
-  const int per_row = wcols / 8;                 // lanes per row
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
     for (int x = 0; x < MI; ++x)
@@ -686,14 +718,19 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    for (int it = lane; it < 32 * per_row; it += kWave) {
+    auto piece = [&](int it, const Added* pre) {
       const int r = it / per_row, c = (it - r * per_row) * 8;
       const int row = wm * RW + i * 32 + r, col = col0 + c;
-      if (row >= mrows || col >= out_w) continue;
+      if (row >= mrows || col >= out_w) return;
+      Added add;
+      if constexpr (MODE == kModeNT) {
+        if (pre) add = *pre;
+        else load_added(row, col, add);
+      }
       float v[8];
       mm_area8(area + r * kRowF + c, v);
       if constexpr (MODE == kModeNT) {
-        if (a.bias) mm_add8<T>(static_cast<const uint16_t*>(a.bias) + col, v);
+        if (a.bias) mm_add8<T>(add.bias, v);
         const uint32_t zoff = (static_cast<uint32_t>(row) * a.ndim + col) * 2;
         if (a.z) {
           mm_put16(mm_pack8<T>(v), z_rs, zoff, stream);
@@ -701,7 +738,7 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
         if (swiglu) {
           float u[8];
           mm_area8(area + r * kRowF + CW / 2 + c, u);
-          if (a.bias) mm_add8<T>(static_cast<const uint16_t*>(a.bias) + half_n + col, u);
+          if (a.bias) mm_add8<T>(add.bias_up, u);
           if (a.z) mm_put16(mm_pack8<T>(u), z_rs, zoff + half_n * 2, stream);
 #pragma unroll
           for (int t = 0; t < 8; ++t) v[t] = act_f32(v[t], 2) * u[t];
@@ -711,14 +748,16 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
         }
       }
       if (MODE == kModeNT && a.residual) {
-        const size_t at = (crow + row) * out_w + col;
         if (a.c_f32) {
-          float w[8];
-          mm_area8(static_cast<const float*>(a.residual) + at, w);
+          const f32x4_t lo = __builtin_bit_cast(f32x4_t, add.res),
+                        hi = __builtin_bit_cast(f32x4_t, add.res_hi);
 #pragma unroll
-          for (int t = 0; t < 8; ++t) v[t] += w[t];
+          for (int t = 0; t < 4; ++t) {
+            v[t] += lo[t];
+            v[4 + t] += hi[t];
+          }
         } else {
-          mm_add8<T>(static_cast<const uint16_t*>(a.residual) + at, v);
+          mm_add8<T>(add.res, v);
         }
       }
       const uint32_t coff = (static_cast<uint32_t>(row) * out_w + col) * (a.c_f32 ? 4 : 2);
@@ -728,6 +767,13 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
       } else {
         mm_put16(mm_pack8<T>(v), c_rs, coff, stream);
       }
+    };
+    if constexpr (kAhead) {
+      static_assert(CW == 32, "two pieces per lane");
+      piece(lane, &ahead[0]);
+      if (!swiglu) piece(lane + kWave, &ahead[1]);
+    } else {
+      for (int it = lane; it < 32 * per_row; it += kWave) piece(it, nullptr);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();

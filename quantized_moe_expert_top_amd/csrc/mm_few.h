@@ -83,6 +83,28 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
   };
 #pragma unroll
   for (int d = 0; d < U; ++d) load(wv + d * WAVES, wr[d], xr[d]);
+  // what is added to the output of piece `it`; the first piece's is requested ahead
+  // of the products
+  const int out_w = swiglu ? half_n : a.ndim, cols = swiglu ? 8 : 16;
+  struct Added {
+    uint16_t bias, bias_up, res;
+    float res_f;
+  };
+  auto load_added = [&](int it, Added& v) {
+    const int r = it / cols, col = n0 + it - r * cols;
+    if (r >= mrows || col >= out_w) return;
+    if (a.bias) {
+      v.bias = static_cast<const uint16_t*>(a.bias)[col];
+      if (swiglu) v.bias_up = static_cast<const uint16_t*>(a.bias)[half_n + col];
+    }
+    if (a.residual) {
+      const size_t at = (static_cast<size_t>(t.p0) + r) * out_w + col;
+      if (a.c_f32) v.res_f = static_cast<const float*>(a.residual)[at];
+      else v.res = static_cast<const uint16_t*>(a.residual)[at];
+    }
+  };
+  Added add;
+  load_added(tid, add);
   for (int s = wv; s < steps; s += U * WAVES) {
 #pragma unroll
     for (int d = 0; d < U; ++d) {
@@ -99,27 +121,26 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
     *reinterpret_cast<f32x4_t*>(&part[wv][i * 16 + l16][kg * 4]) = acc[i];
   __syncthreads();
 
-  const int out_w = swiglu ? half_n : a.ndim, cols = swiglu ? 8 : 16;
   for (int it = tid; it < mrows * cols; it += NTHR) {
     const int r = it / cols, c = it - r * cols, col = n0 + c;
     if (col >= out_w) continue;
+    if (it != tid) load_added(it, add);
     const size_t p = static_cast<size_t>(t.p0) + r;
     float v = 0.0f, g = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) v += part[w][r][c];
-    const uint16_t* bias = static_cast<const uint16_t*>(a.bias);
     uint16_t* z = static_cast<uint16_t*>(a.z);
     float lo, hi;
-    if (bias) {
-      unpack2<T>(bias[col], lo, hi);
+    if (a.bias) {
+      unpack2<T>(add.bias, lo, hi);
       v += lo;
     }
     if (z) z[p * a.ndim + col] = static_cast<uint16_t>(pack2<T>(v, 0.0f));
     if (swiglu) {
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) g += part[w][r][8 + c];
-      if (bias) {
-        unpack2<T>(bias[half_n + col], lo, hi);
+      if (a.bias) {
+        unpack2<T>(add.bias_up, lo, hi);
         g += lo;
       }
       if (z) z[p * a.ndim + half_n + col] = static_cast<uint16_t>(pack2<T>(g, 0.0f));
@@ -130,9 +151,9 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
     const size_t at = p * out_w + col;
     if (a.residual) {
       if (a.c_f32) {
-        v += static_cast<const float*>(a.residual)[at];
+        v += add.res_f;
       } else {
-        unpack2<T>(static_cast<const uint16_t*>(a.residual)[at], lo, hi);
+        unpack2<T>(add.res, lo, hi);
         v += lo;
       }
     }
