@@ -107,6 +107,13 @@ moe::MMArgs mm_args(const moe_mm_shape* s, const int32_t* offsets, const int32_t
 struct MMWs {
   size_t dz, strips, parts, total;
 };
+size_t dx_parts(const moe_mm_shape* s, const moe::MMBackwardPlan& p) {
+  return p.nn_splits > 1 ? align256(static_cast<size_t>(s->rows) * p.nn_splits * s->K * 4) : 0;
+}
+size_t dw_parts(const moe_mm_shape* s, bool grouped, const moe::MMBackwardPlan& p) {
+  const int E = grouped ? s->E : 1;
+  return p.tn_splits > 1 ? align256(static_cast<size_t>(E) * p.tn_splits * s->N * s->K * 4) : 0;
+}
 MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   MMWs w = {};
   size_t at = 0;
@@ -116,18 +123,19 @@ MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   w.strips = at;
   if (!grouped) at += align256(static_cast<size_t>(moe::dz_strips(s->rows, s->N, s->act)) * s->N * 4);
   w.parts = at;
-  const int E = grouped ? s->E : 1, splits = moe::mm_tn_splits(s->rows, E, s->N, s->K);
-  if (splits > 1) at += align256(static_cast<size_t>(E) * splits * s->N * s->K * 4);
-  w.total = at;
+  const moe::MMBackwardPlan p = moe::mm_backward_plan(s->rows, grouped ? s->E : 0, s->N, s->K);
+  w.total = at + dx_parts(s, p) + dw_parts(s, grouped, p);
   return w;
 }
 
 // dx = dz W, dw = dz^T x on the given dz, and `sum` (may be empty)
 moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* x, const void* w,
                              const int32_t* offsets, const int32_t* slot, void* dx, int dx_dtype,
-                             void* dw, int dw_dtype, void* parts, const moe::PartSum& sum,
+                             void* dw, int dw_dtype, uint8_t* parts, const moe::PartSum& sum,
                              hipStream_t st) {
   const bool fp16 = s->dtype == MOE_FP16;
+  if (s->rows == 0) dx = nullptr;
+  const moe::MMBackwardPlan plan = moe::mm_backward_plan(s->rows, offsets ? s->E : 0, s->N, s->K);
   moe::MMArgs nn = mm_args(s, offsets, nullptr);
   nn.A = dz;
   nn.B = w;
@@ -142,34 +150,34 @@ moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* 
   tn.mdim = s->N;
   tn.ndim = s->K;
   tn.c_f32 = dw_dtype == MOE_F32;
-  if (dx && dw && s->rows > 0) {
-    const int pick = moe::mm_pair_pick(s->rows, offsets ? s->E : 0, s->N, s->K);
-    if (pick) return launched(moe::launch_mm_pair(nn, tn, sum, pick, fp16, st), "gradient launch");
+  moe::SplitSum sum_dx = {}, sum_dw = {};
+  if (dw && plan.tn_splits > 1) {
+    tn.splits = plan.tn_splits;
+    tn.C = parts;
+    tn.c_f32 = 1;
+    sum_dw = {reinterpret_cast<const float*>(parts), tn.splits, tn.E,
+              static_cast<long long>(s->N) * s->K, dw, dw_dtype};
+    parts += dw_parts(s, offsets != nullptr, plan);
   }
-  if (sum.out) {
-    const moe_status r = launched(moe::launch_sum_parts(sum, st), "bias gradient launch");
-    if (r) return r;
+  if (dx && plan.nn_splits > 1) {
+    nn.splits = plan.nn_splits;
+    nn.C = parts;
+    nn.c_f32 = 1;
+    sum_dx = {reinterpret_cast<const float*>(parts), nn.splits, 1,
+              static_cast<long long>(s->rows) * s->K, dx, dx_dtype};
   }
-  if (dx && s->rows > 0) {
-    const moe_status r = launched(moe::launch_mm_nn(nn, fp16, st), "row gradient launch");
-    if (r) return r;
+  const bool last = sum_dx.out || sum_dw.out;   // a launch of sums at the end
+  moe_status r;
+  if (dx && dw && plan.pair) {
+    r = launched(moe::launch_mm_pair(nn, tn, last ? moe::PartSum{} : sum, plan.pair, fp16, st),
+                 "gradient launch");
+    if (r || !last) return r;
+  } else {
+    if (dx && (r = launched(moe::launch_mm_nn(nn, plan.nn, fp16, st), "row gradient launch"))) return r;
+    if (dw && (r = launched(moe::launch_mm_tn(tn, plan.tn, fp16, st), "weight gradient launch")))
+      return r;
   }
-  if (dw) {
-    tn.splits = moe::mm_tn_splits(s->rows, tn.E, s->N, s->K);
-    if (tn.splits > 1) {
-      tn.C = parts;
-      tn.c_f32 = 1;
-    }
-    moe_status r = launched(moe::launch_mm_tn(tn, fp16, st), "weight gradient launch");
-    if (r) return r;
-    if (tn.splits > 1) {
-      r = launched(moe::launch_sum_splits(static_cast<const float*>(parts), tn.E, tn.splits,
-                                          static_cast<long long>(s->N) * s->K, dw, dw_dtype, st),
-                   "weight gradient sum launch");
-      if (r) return r;
-    }
-  }
-  return MOE_OK;
+  return launched(moe::launch_sums(sum_dx, sum_dw, sum, st), "gradient sum launch");
 }
 
 }  // namespace

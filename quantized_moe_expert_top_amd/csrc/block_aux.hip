@@ -161,33 +161,39 @@ __global__ __launch_bounds__(256) void dz_flat_kernel(const void* __restrict__ d
   }
 }
 
-__global__ __launch_bounds__(256) void sum_parts_kernel(const PartSum a) {
-  sum_parts_block(a, blockIdx.x);
-}
-
-__global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part,
-                                                         int splits, long long n4, long long total4,
-                                                         void* __restrict__ out, int type) {
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total4;
-       i += static_cast<long long>(gridDim.x) * 256) {
+__device__ __forceinline__ void sum_splits_block(const SplitSum& a, uint32_t bid, uint32_t blocks) {
+  const long long n4 = a.n / 4, total4 = n4 * a.E;
+  for (long long i = static_cast<long long>(bid) * 256 + threadIdx.x; i < total4;
+       i += static_cast<long long>(blocks) * 256) {
     const long long e = i / n4, c = i - e * n4;
-    const float4* p = reinterpret_cast<const float4*>(part) + e * splits * n4 + c;
+    const float4* p = reinterpret_cast<const float4*>(a.part) + e * a.splits * n4 + c;
     float4 v = p[0];
-    for (int s = 1; s < splits; ++s) {
+#pragma unroll 4
+    for (int s = 1; s < a.splits; ++s) {
       const float4 w = p[s * n4];
       v.x += w.x;
       v.y += w.y;
       v.z += w.z;
       v.w += w.w;
     }
-    if (type == 2) {
-      reinterpret_cast<float4*>(out)[i] = v;
-    } else if (type == 0) {
-      reinterpret_cast<uint2*>(out)[i] = make_uint2(pack2<bf16_tag>(v.x, v.y), pack2<bf16_tag>(v.z, v.w));
+    if (a.out_type == 2) {
+      reinterpret_cast<float4*>(a.out)[i] = v;
+    } else if (a.out_type == 0) {
+      reinterpret_cast<uint2*>(a.out)[i] = make_uint2(pack2<bf16_tag>(v.x, v.y), pack2<bf16_tag>(v.z, v.w));
     } else {
-      reinterpret_cast<uint2*>(out)[i] = make_uint2(pack2<fp16_tag>(v.x, v.y), pack2<fp16_tag>(v.z, v.w));
+      reinterpret_cast<uint2*>(a.out)[i] = make_uint2(pack2<fp16_tag>(v.x, v.y), pack2<fp16_tag>(v.z, v.w));
     }
   }
+}
+
+// One launch for all sums of a call: a launch of a few us each would cost more
+// than the sums.
+__global__ __launch_bounds__(256) void sums_kernel(const SplitSum a, const SplitSum b,
+                                                   const PartSum c, uint32_t a_blocks,
+                                                   uint32_t b_blocks) {
+  if (blockIdx.x < a_blocks) sum_splits_block(a, blockIdx.x, a_blocks);
+  else if (blockIdx.x < a_blocks + b_blocks) sum_splits_block(b, blockIdx.x - a_blocks, b_blocks);
+  else sum_parts_block(c, blockIdx.x - a_blocks - b_blocks);
 }
 
 // Rows of a strip: as many strips as fill the chip (about 768 blocks of 512
@@ -237,17 +243,14 @@ hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offs
   return hipGetLastError();
 }
 
-hipError_t launch_sum_parts(const PartSum& sum, hipStream_t s) {
-  sum_parts_kernel<<<sum_parts_blocks(sum), 256, 0, s>>>(sum);
-  return hipGetLastError();
-}
-
-hipError_t launch_sum_splits(const float* part, int E, int splits, long long n, void* out,
-                             int out_type, hipStream_t s) {
-  const long long n4 = n / 4, total4 = n4 * E;
-  const long long blocks = (total4 + 255) / 256;
-  sum_splits_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(
-      part, splits, n4, total4, out, out_type);
+hipError_t launch_sums(const SplitSum& a, const SplitSum& b, const PartSum& c, hipStream_t s) {
+  auto blocks = [](const SplitSum& v) -> uint32_t {
+    const long long n = v.out ? (v.n / 4 * v.E + 255) / 256 : 0;
+    return static_cast<uint32_t>(n < 4096 ? n : 4096);
+  };
+  const uint32_t ab = blocks(a), bb = blocks(b), grid = ab + bb + sum_parts_blocks(c);
+  if (grid == 0) return hipSuccess;
+  sums_kernel<<<grid, 256, 0, s>>>(a, b, c, ab, bb);
   return hipGetLastError();
 }
 

@@ -9,8 +9,8 @@ namespace moe {
 
 struct MMArgs;
 hipError_t launch_mm_nt(const MMArgs& a, bool fp16, hipStream_t s);
-hipError_t launch_mm_nn(const MMArgs& a, bool fp16, hipStream_t s);
-hipError_t launch_mm_tn(const MMArgs& a, bool fp16, hipStream_t s);
+hipError_t launch_mm_nn(const MMArgs& a, int geom, bool fp16, hipStream_t s);
+hipError_t launch_mm_tn(const MMArgs& a, int geom, bool fp16, hipStream_t s);
 // out[n] = sum of part[parts][n] in order; out_type 0 bf16, 1 fp16, 2 float32.
 // out NULL: none.
 struct PartSum {
@@ -19,12 +19,17 @@ struct PartSum {
   void* out;
   int out_type;
 };
-// Both gradients, and a sum, in one launch; pick from mm_pair_pick (E 0: no
-// experts), 0 = apart.
-int mm_pair_pick(int rows, int E, int N, int K);
-hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pick,
+// How the gradients of a product are launched: both in one launch (pair 1 Mid,
+// 2 Small) or apart (0), the geometries (mm_pick_rows's, mm_plan_tn's), the parts of
+// each contraction. The same whichever gradients are asked for, so that one is the
+// same bits alone and with the others.
+struct MMBackwardPlan {
+  int pair, nn, nn_splits, tn, tn_splits;
+};
+MMBackwardPlan mm_backward_plan(int rows, int E, int N, int K);   // E 0: no experts
+// Both gradients, and a sum, in one launch.
+hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
                           bool fp16, hipStream_t s);
-int mm_tn_splits(int rows, int E, int mdim, int ndim);
 
 // dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
 // (part [dz_strips(rows, N, act)][N], may be NULL). offsets NULL: all rows; otherwise
@@ -32,10 +37,17 @@ int mm_tn_splits(int rows, int E, int mdim, int ndim);
 int dz_strips(int rows, int N, int act);
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
                      int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s);
-hipError_t launch_sum_parts(const PartSum& sum, hipStream_t s);
-// the same per expert: out[e][n] = sum_s part[e][s][n] (n a multiple of 4)
-hipError_t launch_sum_splits(const float* part, int E, int splits, long long n, void* out,
-                             int out_type, hipStream_t s);
+// out[e][i] = sum over the parts of part[e][s][i], in order; n values per e (a
+// multiple of 4). out NULL: none.
+struct SplitSum {
+  const float* part;
+  int splits, E;
+  long long n;
+  void* out;
+  int out_type;
+};
+// All of these sums (those that there are) in one launch.
+hipError_t launch_sums(const SplitSum& a, const SplitSum& b, const PartSum& c, hipStream_t s);
 
 struct NormArgs {
   const void* r;        // forward: r; backward: r_out

@@ -183,7 +183,7 @@ struct MMArgs {
   int act;
   int c_f32;             // C is float32 (else T)
   int stream_out;        // C and z are past what the caches can keep
-  int splits;            // TN: parts of an expert's rows, each to its own C
+  int splits;            // parts of the contraction, each to its own C (TN; NN without offsets)
   int nt;                // n tiles
   int mt;                // TN: m tiles
   int xm;                // TN: m slices of an expert's tiles over the XCDs (1, 2, 4, 8), or 0
@@ -375,7 +375,7 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
   // ---- the tile
   int e = 0, m0 = 0, n0 = 0;        // expert, first C row and column of the tile
   int mrows = 0;                    // rows of C in the tile
-  int k_begin = 0, k_end = 0;       // TN: rows contracted over
+  int k_begin = 0, k_end = 0;       // what is contracted over (TN: rows)
   int split = 0;
   if constexpr (MODE == kModeTN) {
     int es, mi, ni;
@@ -419,7 +419,17 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
     k_end = __builtin_amdgcn_readfirstlane(min(k_begin + part, hi));
   } else {
     MMTile t;
-    if (!mm_find_tile<BM, NTHR>(a.offsets, a.rows, a.E, a.nt, sm_tile, bid, t)) return;
+    const int nts = MODE == kModeNN ? a.nt * a.splits : a.nt;   // a part's tiles: more columns
+    if (!mm_find_tile<BM, NTHR>(a.offsets, a.rows, a.E, nts, sm_tile, bid, t)) return;
+    if constexpr (MODE == kModeNN) {
+      split = __builtin_amdgcn_readfirstlane(t.nt / a.nt);
+      t.nt -= split * a.nt;
+      const int part = ((a.kdim + a.splits - 1) / a.splits + BK - 1) / BK * BK;
+      k_begin = min(split * part, a.kdim);
+      k_end = min(k_begin + part, a.kdim);
+    } else {
+      k_end = a.kdim;
+    }
     e = t.e;
     m0 = t.p0;
     mrows = t.p1 - t.p0;
@@ -484,16 +494,17 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
       bkc[v] = k;
     }
   }
-  const int klen = MODE == kModeTN ? k_end - k_begin : a.kdim;
+  const int klen = k_end - k_begin;
   const int steps = (klen + BK - 1) / BK;
   const int wvu = __builtin_amdgcn_readfirstlane(wv);
   const uint8_t* wexp = Bb + static_cast<size_t>(e) * a.kdim * a.ndim * esz;   // NT, NN: W_e
 
   // Resources whose extent does not move with k
   const uint32_t x_bytes = MODE == kModeNT && gather ? static_cast<uint32_t>(a.x_rows) * kb
-                                                     : static_cast<uint32_t>(mrows) * kb;
+                                                     : static_cast<uint32_t>(mrows) * kb - k_begin * 2;
   const __amdgpu_buffer_rsrc_t a_fix = buffer_rsrc(
-      MODE == kModeNT && gather ? Ab : Ab + static_cast<size_t>(m0) * kb, kAK ? x_bytes : 0);
+      MODE == kModeNT && gather ? Ab : Ab + static_cast<size_t>(m0) * kb + (kAK ? k_begin * 2 : 0),
+      kAK ? x_bytes : 0);
   const __amdgpu_buffer_rsrc_t b_fix =
       buffer_rsrc(kBK ? wexp : Bb, kBK ? static_cast<uint32_t>(a.ndim) * kb
                                        : MODE == kModeTN && gather
@@ -656,7 +667,9 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
   const int out_w = swiglu ? half_n : a.ndim;
   const int wcols = swiglu ? CW / 2 : CW;        // output columns of the wave
   const size_t crow = static_cast<size_t>(m0) +
-                      (MODE == kModeTN ? (static_cast<size_t>(e) * a.splits + split) * a.mdim : 0);
+                      (MODE == kModeTN   ? (static_cast<size_t>(e) * a.splits + split) * a.mdim
+                       : MODE == kModeNN ? static_cast<size_t>(split) * a.rows
+                                         : 0);
   const int col0 = n0 + wn * wcols;
   const int per_row = wcols / 8;                 // lanes per row
   // what is added to 8 columns of a row (NT), as it is stored

@@ -162,6 +162,16 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
   }
 }
 
+// us of a dense product: blocks of 16 MT rows x 16 columns, `step` per 64 k for the
+// first 256 of them and a fifth more for each further 256 (401 x 288 x 2952: 16 rows
+// 10.8 us timed, 11.0 here; 32 rows 8.9, 9.0; 64 x 64 tiles 12.4).
+inline double mm_few_cost(int mt, int rows, int ndim, int kdim) {
+  const double blocks = static_cast<double>((rows + 16 * mt - 1) / (16 * mt)) * ((ndim + 15) / 16);
+  const double step = mt == 1 ? 0.072 : 0.104, start = mt == 1 ? 3.4 : 4.2;
+  const double rounds = __builtin_ceil(blocks / 256);
+  return start + (kdim + 63) / 64 * step * (1.0 + 1.2 * (rounds - 1)) + 0.5 * (rounds - 1);
+}
+
 template <class T, int MT, int WAVES, int U>
 hipError_t mm_few_launch(MMArgs a, hipStream_t s) {
   const bool swiglu = a.act == kActSwiglu;

@@ -29,15 +29,18 @@ using MMLong = MMGeom<128, 256, 2, 2, 32, 3, 2>;
 //       grouped, 128 experts, 32768 x 1536 x 2048   Big 297 (306)   Mid 302 (320)
 //       grouped, 128 experts, 32768 x 2048 x 768    Big 172 (205)   Mid 205 (214)
 //   TN  1536 x 2048 x 4096   Big 83 (85)     Mid 45 (41)    Small 52 (50)
+// `dense` stands for `full` where no experts' weights have to come from memory:
+//   NT  6115 x 5728 x 176    Big 46 (51)     Mid 46 (42)    Wide 39 (34)    Small 53 (51)
+//       5549 x 384 x 5760    Big 110 (115)   Mid 62 (64)    Wide 55 (55)    Small 59 (55)
 struct MMCost {
   int bm, bn, slots;
-  double s1, s2, s3, full, part;
+  double s1, s2, s3, full, part, dense;
 };
-constexpr MMCost kMMBigCost = {256, 256, 256, 1.12, 1.64, 1.64, 9.0, 9.0};
-constexpr MMCost kMMMidCost = {128, 128, 512, 0.57, 0.65, 0.96, 9.0, 4.0};
-constexpr MMCost kMMWideCost = {64, 128, 512, 0.30, 0.36, 0.65, 6.5, 3.8};
-constexpr MMCost kMMSmallCost = {64, 64, 512, 0.20, 0.23, 0.40, 5.0, 3.5};
-constexpr MMCost kMMLongCost = {128, 256, 512, 1.00, 1.20, 1.90, 11.0, 5.0};
+constexpr MMCost kMMBigCost = {256, 256, 256, 1.12, 1.64, 1.64, 9.0, 9.0, 14.0};
+constexpr MMCost kMMMidCost = {128, 128, 512, 0.62, 0.66, 0.96, 9.0, 4.0, 7.5};
+constexpr MMCost kMMWideCost = {64, 128, 512, 0.30, 0.36, 0.65, 6.5, 3.8, 2.3};
+constexpr MMCost kMMSmallCost = {64, 64, 512, 0.20, 0.23, 0.40, 5.0, 3.5, 1.7};
+constexpr MMCost kMMLongCost = {128, 256, 512, 1.00, 1.20, 1.90, 11.0, 5.0, 12.0};
 
 // m tiles of row blocks: of `rows` rows in one block (E = 0), or spread over E
 // experts, where about half a tile per expert in use is left over and none has
@@ -47,14 +50,19 @@ inline double mm_row_tiles(int bm, int rows, int E) {
   const double act = rows < E ? rows : E, n = static_cast<double>(rows) / bm + 0.5 * act;
   return n > act ? n : act;
 }
-inline double mm_cost(const MMCost& c, double tiles, double stages) {
+// Dense: `epi` us per 65536 results of a CU for activations.
+inline double mm_cost(const MMCost& c, double tiles, double stages, bool dense = false,
+                      double epi = 0.0) {
   const double full = __builtin_floor(tiles / c.slots), rem = tiles - full * c.slots;
-  double cost = full * (stages * c.s3 + c.full);
+  const double act = epi * c.bm * c.bn / 65536;
+  double cost = full * (stages * c.s3 + (dense ? c.dense + act * c.slots / 256 : c.full));
   if (rem > 0) {
+    // a CU with two blocks is done last, however few of them there are
     const double s = rem <= 64    ? c.s1
                      : rem <= 256 ? c.s1 + (c.s2 - c.s1) * (rem - 64) / 192
+                     : dense      ? 0.87 * c.s3
                                   : c.s2 + (c.s3 - c.s2) * (rem - 256) / (c.slots - 256);
-    cost += stages * s + c.part;
+    cost += stages * s + c.part + act * (rem > 256 ? 2 : 1);
   }
   return cost;
 }
@@ -66,7 +74,9 @@ struct MMPick {
   int geom;
   double cost;   // us
 };
-inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim) {
+inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim, int act = 0) {
+  // 8192 x 4096 x 1024: silu + 9 us in Big, gelu + 18; Mid + 7 and + 14 by this
+  const double epi = E != 0 ? 0.0 : act == 3 ? 12.0 : act == 2 || act == kActSwiglu ? 6.0 : 0.0;
   const MMCost* const table[5] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost,
                                   &kMMLongCost};
   const bool low = E > 1 && rows <= 96LL * (rows < E ? rows : E);
@@ -75,7 +85,7 @@ inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim) {
     const MMCost& c = *table[i];
     if (low && c.bm > 64) continue;
     const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * ((ndim + c.bn - 1) / c.bn),
-                                (kdim + 63) / 64);
+                                (kdim + 63) / 64, E == 0, epi);
     if (cost < best.cost) best = {i, cost};
   }
   return best;
@@ -113,10 +123,10 @@ long long mm_prepare(MMArgs& a) {
     }
     mm_set_stream(a, static_cast<long long>(a.E) * a.splits * a.mdim * a.ndim);
   } else {
-    mm_set_stream(a, static_cast<long long>(a.rows) * (swiglu ? a.ndim / 2 : a.ndim));
+    mm_set_stream(a, static_cast<long long>(a.rows) * a.splits * (swiglu ? a.ndim / 2 : a.ndim));
     // an upper bound over all ways to cut the rows: a partial tile per expert
     const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
-    tiles = (a.rows / G::BM + partial) * a.nt;
+    tiles = (a.rows / G::BM + partial) * a.nt * a.splits;
   }
   return (tiles + 7) / 8 * 8;
 }
@@ -143,7 +153,7 @@ template <class T, int MODE, class G>
 hipError_t mm_launch(MMArgs a, hipStream_t s) {
   const long long grid = mm_prepare<MODE, G>(a);
   if (grid == 0) return hipSuccess;
-  const long long each = MODE == kModeTN ? 0 : (a.rows / G::BM + 1LL) * a.nt;
+  const long long each = MODE == kModeTN ? 0 : (a.rows / G::BM + 1LL) * a.nt * a.splits;
   if (!mm_fits(grid, G::kThreads, each, a.E)) return hipErrorInvalidConfiguration;
   static MMReady ready;
   const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_kernel<T, MODE, G>), G::kLds);

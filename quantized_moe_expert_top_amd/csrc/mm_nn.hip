@@ -6,8 +6,8 @@ namespace moe {
 namespace {
 
 template <class T>
-hipError_t launch(const MMArgs& a, hipStream_t s) {
-  switch (mm_pick_rows(a.rows, a.offsets ? a.E : 0, a.ndim, a.kdim).geom) {
+hipError_t launch(const MMArgs& a, int geom, hipStream_t s) {
+  switch (geom) {
     case 0: return mm_launch<T, kModeNN, MMBig>(a, s);
     case 1: return mm_launch<T, kModeNN, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNN, MMWide>(a, s);
@@ -18,8 +18,8 @@ hipError_t launch(const MMArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_mm_nn(const MMArgs& a, bool fp16, hipStream_t s) {
-  return fp16 ? launch<fp16_tag>(a, s) : launch<bf16_tag>(a, s);
+hipError_t launch_mm_nn(const MMArgs& a, int geom, bool fp16, hipStream_t s) {
+  return fp16 ? launch<fp16_tag>(a, geom, s) : launch<bf16_tag>(a, geom, s);
 }
 
 }  // namespace moe

@@ -26,7 +26,7 @@ template <class T, class G>
 hipError_t launch(MMArgs nn, MMArgs tn, const PartSum& sum, hipStream_t s) {
   const long long tb = mm_prepare<kModeTN, G>(tn), nb = mm_prepare<kModeNN, G>(nn),
                   grid = tb + nb + sum_parts_blocks(sum);
-  if (!mm_fits(grid, G::kThreads, (nn.rows / G::BM + 1LL) * nn.nt, nn.E))
+  if (!mm_fits(grid, G::kThreads, (nn.rows / G::BM + 1LL) * nn.nt * nn.splits, nn.E))
     return hipErrorInvalidConfiguration;
   static MMReady ready;
   const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_pair_kernel<T, G>), G::kLds);
@@ -51,34 +51,70 @@ double pair_cost(const MMCost& c, double tn_tiles, double tn_stages, double nn_t
 
 }  // namespace
 
-// 1 Mid, 2 Small, 0 apart: where one launch is expected to beat two (3 us for the
-// second launch and its start).
-int mm_pair_pick(int rows, int E, int N, int K) {
+// The cheapest way: apart, with 3 us for the second launch and its start, or in one
+// launch; contractions cut where that fills the chip (only without experts in the
+// row gradient; with experts only apart).
+static MMBackwardPlan plan_of(int rows, int E, int N, int K) {
   const bool grouped = E > 0;
-  const TNPlan tn = mm_plan_tn(rows, grouped ? E : 1, N, K);
-  const double apart = tn.cost + mm_pick_rows(rows, E, K, N).cost + 3.0;
   const int groups = grouped ? E : 1;
-  double stages = static_cast<double>(rows) / groups / 64 + (grouped ? 0.5 : 0.0);
-  if (stages < 1.0) stages = 1.0;
-  int best = 0;
-  double at = apart;
+  const MMPick nn1 = mm_pick_rows(rows, E, K, N);
+  MMPlan nn[2] = {{nn1.geom, 1, nn1.cost}, {0, 1, 1e300}};
+  if (!grouped) nn[1] = mm_plan_nn_split(rows, K, N);
+  const MMPlan tn[2] = {mm_plan_tn(rows, groups, N, K, false), mm_plan_tn(rows, groups, N, K, true)};
+  MMBackwardPlan best = {0, nn[0].geom, 1, tn[0].geom, 1};
+  double at = 1e300;
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j) {
+      const double cost = nn[i].cost + tn[j].cost + 3.0 + (i || j ? kMMSplitLaunch : 0.0);
+      if (cost < at) {
+        at = cost;
+        best = {0, nn[i].geom, nn[i].splits, tn[j].geom, tn[j].splits};
+      }
+    }
+  double tn_stages = static_cast<double>(rows) / groups / 64 + (grouped ? 0.5 : 0.0);
+  if (tn_stages < 1.0) tn_stages = 1.0;
+  const double nn_stages = (N + 63) / 64;
   const MMCost* const table[2] = {&kMMMidCost, &kMMSmallCost};
   for (int i = 0; i < 2; ++i) {
     const MMCost& c = *table[i];
     const double kt = (K + c.bn - 1) / c.bn;
-    const double cost = pair_cost(c, groups * ((N + c.bm - 1) / c.bm) * kt, stages,
-                                  mm_row_tiles(c.bm, rows, E) * kt, (N + 63) / 64);
-    if (cost < at) {
-      at = cost;
-      best = i + 1;
-    }
+    const double tn_tiles = groups * static_cast<double>((N + c.bm - 1) / c.bm) * kt,
+                 nn_tiles = mm_row_tiles(c.bm, rows, E) * kt;
+    for (int a = 1; a == 1 || (!grouped && a <= 32 && nn_stages >= 4.0 * a); a *= 2)
+      for (int b = 1; b == 1 || (!grouped && b <= 32 && tn_stages >= 4.0 * b); b *= 2) {
+        const double cost = pair_cost(c, tn_tiles * b, tn_stages / b, nn_tiles * a, nn_stages / a) +
+                            mm_split_cost(static_cast<double>(rows) * K, a) +
+                            mm_split_cost(static_cast<double>(N) * K, b) +
+                            (a > 1 || b > 1 ? kMMSplitLaunch : 0.0);
+        if (cost < at) {
+          at = cost;
+          best = {i + 1, i == 0 ? 1 : 3, a, i == 0 ? 2 : 3, b};
+        }
+      }
   }
   return best;
 }
 
-hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pick,
+MMBackwardPlan mm_backward_plan(int rows, int E, int N, int K) {
+  // this thread's last plans: one takes some hundred evaluations, about as long as
+  // a launch
+  struct Kept {
+    bool set;
+    int rows, E, N, K;
+    MMBackwardPlan plan;
+  };
+  static thread_local Kept kept[16];
+  const uint32_t h = (static_cast<uint32_t>(rows) * 2654435761u) ^ (static_cast<uint32_t>(N) * 40503u) ^
+                     (static_cast<uint32_t>(K) * 9973u) ^ (static_cast<uint32_t>(E) * 31u);
+  Kept& k = kept[(h ^ (h >> 15)) & 15];
+  if (!k.set || k.rows != rows || k.E != E || k.N != N || k.K != K)
+    k = {true, rows, E, N, K, plan_of(rows, E, N, K)};
+  return k.plan;
+}
+
+hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
                           bool fp16, hipStream_t s) {
-  if (pick == 1)
+  if (pair == 1)
     return fp16 ? launch<fp16_tag, MMMid>(nn, tn, sum, s) : launch<bf16_tag, MMMid>(nn, tn, sum, s);
   return fp16 ? launch<fp16_tag, MMSmall>(nn, tn, sum, s) : launch<bf16_tag, MMSmall>(nn, tn, sum, s);
 }

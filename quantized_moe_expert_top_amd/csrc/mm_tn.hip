@@ -6,8 +6,8 @@ namespace moe {
 namespace {
 
 template <class T>
-hipError_t launch(const MMArgs& a, hipStream_t s) {
-  switch (mm_plan_tn(a.rows, a.E, a.mdim, a.ndim).geom) {
+hipError_t launch(const MMArgs& a, int geom, hipStream_t s) {
+  switch (geom) {
     case 0: return mm_launch<T, kModeTN, MMBig>(a, s);
     case 1: return mm_launch<T, kModeTN, MMTall>(a, s);
     case 2: return mm_launch<T, kModeTN, MMMid>(a, s);
@@ -17,10 +17,8 @@ hipError_t launch(const MMArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int mm_tn_splits(int rows, int E, int mdim, int ndim) { return mm_plan_tn(rows, E, mdim, ndim).splits; }
-
-hipError_t launch_mm_tn(const MMArgs& a, bool fp16, hipStream_t s) {
-  return fp16 ? launch<fp16_tag>(a, s) : launch<bf16_tag>(a, s);
+hipError_t launch_mm_tn(const MMArgs& a, int geom, bool fp16, hipStream_t s) {
+  return fp16 ? launch<fp16_tag>(a, geom, s) : launch<bf16_tag>(a, geom, s);
 }
 
 }  // namespace moe
