@@ -3,10 +3,10 @@
 //   dy[pos(t, j)] = w_tj dout_t        dw_tj = <dout_t, y[pos(t, j)]>
 //   dlogits[t, id_tj] = w_tj (dw_tj - sum_i w_ti dw_ti),  0 elsewhere
 //
-// Bound by the bytes of y and dy. A block takes a token, a wave one pick at a
-// time over the whole row, so a pick's dot product is one wave sum in a fixed
-// order and all k rows are in flight at once; dout comes from the caches after
-// its first read.
+// Bound by the bytes of y and dy. A block takes a token, a wave (16 lanes where
+// rows are short) one pick at a time over the whole row, so a pick's dot product is
+// one sum in a fixed order and the rows are in flight at once; dout comes from the
+// caches after its first read.
 #include "launch_block.h"
 #include "mm.h"
 
@@ -34,7 +34,17 @@ __device__ __forceinline__ void store_dy(void* dy, size_t at, const float (&v)[8
   }
 }
 
-template <int DY, bool STREAM>
+// Sum over LPG neighbouring lanes, in a fixed order; each gets it.
+template <int LPG>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (LPG == kWave) return wave_sum_f32(v);
+#pragma unroll
+  for (int d = LPG / 2; d > 0; d /= 2) v += __shfl_xor(v, d, kWave);
+  return v;
+}
+
+// LPG lanes per pick: 16 for rows of up to 256 values, else a wave.
+template <int DY, bool STREAM, int LPG>
 __global__ __launch_bounds__(512) void combine_backward_kernel(
     const float* __restrict__ dout, const float* __restrict__ y, const int* __restrict__ slot_pos,
     const int* __restrict__ ids, const float* __restrict__ w, long long R, int H, int E, int k,
@@ -42,12 +52,12 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(
   __shared__ float sdw[kMaxPicks];
   __shared__ float swt[kMaxPicks];
   __shared__ int sid[kMaxPicks];
-  const int t = blockIdx.x, lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
-  const int waves = blockDim.x >> 6;
+  const int t = blockIdx.x, lane = threadIdx.x % LPG, grp = threadIdx.x / LPG;
+  const int groups = blockDim.x / LPG;
   const int C = H / 8;
   const float* drow = dout + static_cast<size_t>(t) * H;
   const bool need_dot = dw != nullptr || dlogits != nullptr;
-  for (int j = wv; j < k; j += waves) {
+  for (int j = grp; j < k; j += groups) {
     const size_t f = static_cast<size_t>(t) * k + j;
     long long p = slot_pos[f];
     p = p < 0 ? 0 : p >= R ? R - 1 : p;
@@ -55,7 +65,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(
     const size_t row = static_cast<size_t>(p) * H;
     float dot = 0.0f;
 #pragma unroll 4
-    for (int c = lane; c < C; c += kWave) {
+    for (int c = lane; c < C; c += LPG) {
       const float4* d4 = reinterpret_cast<const float4*>(drow + c * 8);
       const float4 d0 = d4[0], d1 = d4[1];
       if (need_dot) {
@@ -71,7 +81,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(
       }
     }
     if (need_dot) {
-      dot = wave_sum_f32(dot);
+      dot = lanes_sum<LPG>(dot);
       if (lane == 0) {
         if (dw) dw[f] = dot;
         sdw[j] = dot;
@@ -98,24 +108,33 @@ hipError_t launch_combine_backward(const float* dout, const float* y, const int*
                                    void* dy, int dy_type, float* dw, float* dlogits,
                                    hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const int threads = k > 4 ? 512 : k > 2 ? 256 : k > 1 ? 128 : 64;
+  // 5351 tokens x 9 picks x 120: 28 us with a wave per pick, 12 with 16 lanes
+  const int lpg = H <= 256 ? 16 : kWave, most = 512 / lpg;
+  const int passes = (k + most - 1) / most, groups = (k + passes - 1) / passes;
+  const int threads = (groups * lpg + kWave - 1) / kWave * kWave;
   const long long R = static_cast<long long>(T) * k;
-  const bool stream = dy && R * H * (dy_type == 2 ? 4 : 2) > (32LL << 20);
-  auto launch = [&](auto dyc) {
-    constexpr int DY = decltype(dyc)::value;
+  const bool stream = dy && R * H * (dy_type == 2 ? 4 : 2) > (32LL << 20) &&
+                      H % 64 == 0;   // rows of whole cache lines
+  auto launch = [&](auto dyc, auto lpgc) {
+    constexpr int DY = decltype(dyc)::value, LPG = decltype(lpgc)::value;
     // one launch holds less than 2^32 threads: 2^22 tokens of 512
     constexpr int kLaunchTokens = 1 << 22;
     for (long long t0 = 0; t0 < T; t0 += kLaunchTokens) {
       const unsigned n = static_cast<unsigned>(T - t0 < kLaunchTokens ? T - t0 : kLaunchTokens);
-      const auto run = stream ? &combine_backward_kernel<DY, true> : &combine_backward_kernel<DY, false>;
+      const auto run = stream ? &combine_backward_kernel<DY, true, LPG>
+                              : &combine_backward_kernel<DY, false, LPG>;
       run<<<n, threads, 0, s>>>(dout + t0 * H, y, slot_pos + t0 * k, ids ? ids + t0 * k : nullptr,
                                 w + t0 * k, R, H, E, k, dy, dw ? dw + t0 * k : nullptr,
                                 dlogits ? dlogits + t0 * E : nullptr);
     }
   };
-  if (dy_type == 0) launch(std::integral_constant<int, 0>{});
-  else if (dy_type == 1) launch(std::integral_constant<int, 1>{});
-  else launch(std::integral_constant<int, 2>{});
+  auto typed = [&](auto lpgc) {
+    if (dy_type == 0) launch(std::integral_constant<int, 0>{}, lpgc);
+    else if (dy_type == 1) launch(std::integral_constant<int, 1>{}, lpgc);
+    else launch(std::integral_constant<int, 2>{}, lpgc);
+  };
+  if (lpg == 16) typed(std::integral_constant<int, 16>{});
+  else typed(std::integral_constant<int, 64>{});
   return hipGetLastError();
 }
 

@@ -91,10 +91,12 @@ inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim, int act = 0) {
   return best;
 }
 
-// Results of more than the L2s' 32 MB go past them (see mm_put16).
-inline void mm_set_stream(MMArgs& a, long long values) {
-  const long long bytes = values * (a.c_f32 ? 4 : 2) + (a.z ? 2LL * a.rows * a.ndim : 0);
-  a.stream_out = bytes > (32LL << 20);
+// Results of more than the L2s' 32 MB go past them (see mm_put16), if their rows are
+// whole cache lines: lines that two tiles write in part would be written twice
+// (53 experts x 3552 x 232 bf16: 42 us with the hint, 21 without).
+inline void mm_set_stream(MMArgs& a, long long rows, long long cols) {
+  const long long row = cols * (a.c_f32 ? 4 : 2), z_row = a.z ? 2LL * a.ndim : 0;
+  a.stream_out = rows * (row + z_row) > (32LL << 20) && row % 128 == 0 && z_row % 128 == 0;
 }
 
 // Fills in what the kernel needs of the geometry; returns the grid (a multiple of 8).
@@ -121,9 +123,9 @@ long long mm_prepare(MMArgs& a) {
         }
       }
     }
-    mm_set_stream(a, static_cast<long long>(a.E) * a.splits * a.mdim * a.ndim);
+    mm_set_stream(a, static_cast<long long>(a.E) * a.splits * a.mdim, a.ndim);
   } else {
-    mm_set_stream(a, static_cast<long long>(a.rows) * a.splits * (swiglu ? a.ndim / 2 : a.ndim));
+    mm_set_stream(a, static_cast<long long>(a.rows) * a.splits, swiglu ? a.ndim / 2 : a.ndim);
     // an upper bound over all ways to cut the rows: a partial tile per expert
     const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
     tiles = (a.rows / G::BM + partial) * a.nt * a.splits;

@@ -626,8 +626,8 @@ NormArgs rows_from(NormArgs a, int t0, int rows) {
   return a;
 }
 
-bool streams(const NormArgs& a, long long bytes_per_value) {
-  return static_cast<long long>(a.T) * a.H * bytes_per_value > (32LL << 20);
+bool streams(const NormArgs& a, long long bytes_per_value) {   // rows of whole cache lines
+  return static_cast<long long>(a.T) * a.H * bytes_per_value > (32LL << 20) && a.H % 64 == 0;
 }
 
 }  // namespace

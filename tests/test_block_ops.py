@@ -486,7 +486,8 @@ def test_block_norm_zero_tokens():
 
 # ------------------------------------------------------------------ combine --
 @pytest.mark.parametrize("T,H,E,k", [(1, 8, 1, 1), (3, 520, 5, 2), (2, 7168, 256, 8), (64, 2048, 128, 8),
-                                     (17, 1032, 1024, 32), (130, 264, 40, 5), (9, 16, 16, 13)])
+                                     (17, 1032, 1024, 32), (130, 264, 40, 5), (9, 16, 16, 13),
+                                     (200, 120, 71, 9), (33, 256, 64, 16), (7, 248, 500, 31)])
 @pytest.mark.parametrize("t", [BF, HF, F32])
 def test_combine_backward(T, H, E, k, t):
     import quantized_moe_expert_top_amd as moe
@@ -872,6 +873,11 @@ GEOMETRIES = [
     (8200, 4104, 7184, 0), (2500, 264, 4112, 0), (4093, 2048, 1536, 0), (1100, 96, 2048, 0),
     (40000, 72, 80, 0), (700, 2056, 1040, 0), (8200, 4104, 7184, 3), (4000, 2056, 1040, 6),
     (9000, 1032, 2064, 3), (300, 64, 2064, 40), (12000, 520, 2064, 3), (16000, 1032, 2064, 60),
+    # few results of long contractions: cut in parts, or over a block's waves
+    (3, 464, 4704, 0), (946, 256, 5712, 0), (30, 2048, 4112, 0), (401, 5624, 128, 0),
+    (70, 96, 2000, 0), (3698, 104, 1152, 0), (200, 2952, 112, 0),
+    # rows of dw that are no whole cache lines, more than the caches hold
+    (25, 232, 3552, 53),
 ]
 
 
