@@ -20,18 +20,17 @@ using MMLong = MMGeom<128, 256, 2, 2, 32, 3, 2>;
 
 // What a geometry costs, in us on one MI355X: a round of resident blocks takes
 // `s1`, `s2` or `s3` per 64-k stage with 64, 256 or `slots` blocks at work (fewer
-// blocks, more of the caches' rate for each; between them in proportion), and
-// `full` (a full round) or `part` (the last one) for first loads and epilogues.
-// Fitted; what the fit says and, in brackets, what was timed:
-//   NT  8192 x 4096 x 7168   Big 385 (376)   Mid 466 (462)
-//       4096 x 2048 x 1536   Big 43 (38)     Mid 32 (28)    Wide 44 (36)    Small 59 (42)
-//       512 x 2048 x 768     Mid 11 (10.7)   Wide 7.8 (8.1) Small 6.3 (6.5)
+// blocks, more of the caches' rate for each), and `full` (a full round with experts'
+// weights from memory; `dense` without) or `part` (the last round) for first loads
+// and epilogues. Fitted; what the fit says and, in brackets, what was timed:
+//   NT  8192 x 4096 x 7168   Big 395 (376)   Mid 460 (462)
+//       4096 x 2048 x 1536   Big 40 (44)     Mid 31 (31)    Wide 36 (35)    Small 45 (42)
+//       6115 x 5728 x 176    Big 46 (51)     Mid 46 (42)    Wide 39 (34)    Small 53 (51)
+//       5549 x 384 x 5760    Big 110 (115)   Mid 62 (64)    Wide 55 (55)    Small 59 (55)
+//       512 x 2048 x 768     Mid 11 (10.7)   Wide 7.6 (8.1) Small 6.3 (6.5)
 //       grouped, 128 experts, 32768 x 1536 x 2048   Big 297 (306)   Mid 302 (320)
 //       grouped, 128 experts, 32768 x 2048 x 768    Big 172 (205)   Mid 205 (214)
 //   TN  1536 x 2048 x 4096   Big 83 (85)     Mid 45 (41)    Small 52 (50)
-// `dense` stands for `full` where no experts' weights have to come from memory:
-//   NT  6115 x 5728 x 176    Big 46 (51)     Mid 46 (42)    Wide 39 (34)    Small 53 (51)
-//       5549 x 384 x 5760    Big 110 (115)   Mid 62 (64)    Wide 55 (55)    Small 59 (55)
 struct MMCost {
   int bm, bn, slots;
   double s1, s2, s3, full, part, dense;
