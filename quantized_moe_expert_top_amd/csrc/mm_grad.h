@@ -46,10 +46,11 @@ inline MMPlan mm_plan_tn(int rows, int E, int mdim, int ndim, bool split) {
 }
 // NN without experts, in several parts: geometries of mm_pick_rows.
 inline MMPlan mm_plan_nn_split(int rows, int ndim, int kdim) {
-  const MMCost* const table[4] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost};
+  const MMCost* const table[6] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost,
+                                  &kMMLongCost, &kMMDeepCost};
   MMPlan best = {0, 1, 1e300};
   const double stages = (kdim + 63) / 64;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 6; ++i) {
     const MMCost& c = *table[i];
     const double tiles = mm_row_tiles(c.bm, rows, 0) * ((ndim + c.bn - 1) / c.bn);
     for (int s = 2; s <= 32 && stages >= 4.0 * s; s *= 2) {

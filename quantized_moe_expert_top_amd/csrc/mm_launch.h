@@ -17,6 +17,10 @@ using MMSmall = MMGeom<64, 64, 2, 2, 64, 4, 2>;    // 4 waves, two blocks per CU
 // few stages it wins (128 experts, 32768 rows x 2048 x 768 to float32: 215 against
 // 240 us; its row gradient 150 against 167).
 using MMLong = MMGeom<128, 256, 2, 2, 32, 3, 2>;
+// 8 waves, one block per CU, four stages: where a dense product has too few tiles
+// for two blocks per CU a block alone has to keep enough loads in flight (1219 x 1728
+// x 5120: 40 us, Mid 60, Wide 50; 5549 x 384 x 5760: 40, Mid 63, Wide 53).
+using MMDeep = MMGeom<128, 128, 2, 4, 64, 4, 2>;
 
 // What a geometry costs, in us on one MI355X: a round of resident blocks takes
 // `s1`, `s2` or `s3` per 64-k stage with 64, 256 or `slots` blocks at work (fewer
@@ -40,6 +44,7 @@ constexpr MMCost kMMMidCost = {128, 128, 512, 0.62, 0.66, 0.96, 9.0, 4.0, 7.5};
 constexpr MMCost kMMWideCost = {64, 128, 512, 0.30, 0.36, 0.65, 6.5, 3.8, 2.3};
 constexpr MMCost kMMSmallCost = {64, 64, 512, 0.20, 0.23, 0.40, 5.0, 3.5, 1.7};
 constexpr MMCost kMMLongCost = {128, 256, 512, 1.00, 1.20, 1.90, 11.0, 5.0, 12.0};
+constexpr MMCost kMMDeepCost = {128, 128, 256, 0.41, 0.61, 0.61, 6.0, 4.0, 4.5};
 
 // m tiles of row blocks: of `rows` rows in one block (E = 0), or spread over E
 // experts, where about half a tile per expert in use is left over and none has
@@ -66,7 +71,7 @@ inline double mm_cost(const MMCost& c, double tiles, double stages, bool dense =
   return cost;
 }
 // The cheapest geometry for row-grouped products (NT, NN): 0 Big, 1 Mid, 2 Wide,
-// 3 Small, 4 Long. Experts of few rows are bound by streaming their weights, which
+// 3 Small, 4 Long, 5 Deep (dense only). Experts of few rows are bound by streaming their weights, which
 // the low tiles keep most loads in flight for (128 experts x 1536 x 2048: 8192 rows
 // Wide 181, Long 207, Mid 216, Big 249 us; 4096 rows 166, -, 189, 200).
 struct MMPick {
@@ -76,11 +81,11 @@ struct MMPick {
 inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim, int act = 0) {
   // 8192 x 4096 x 1024: silu + 9 us in Big, gelu + 18; Mid + 7 and + 14 by this
   const double epi = E != 0 ? 0.0 : act == 3 ? 12.0 : act == 2 || act == kActSwiglu ? 6.0 : 0.0;
-  const MMCost* const table[5] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost,
-                                  &kMMLongCost};
+  const MMCost* const table[6] = {&kMMBigCost, &kMMMidCost, &kMMWideCost, &kMMSmallCost,
+                                  &kMMLongCost, &kMMDeepCost};
   const bool low = E > 1 && rows <= 96LL * (rows < E ? rows : E);
   MMPick best = {0, 1e300};
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < (E == 0 ? 6 : 5); ++i) {
     const MMCost& c = *table[i];
     if (low && c.bm > 64) continue;
     const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * ((ndim + c.bn - 1) / c.bn),

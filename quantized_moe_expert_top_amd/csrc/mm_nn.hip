@@ -12,7 +12,8 @@ hipError_t launch(const MMArgs& a, int geom, hipStream_t s) {
     case 1: return mm_launch<T, kModeNN, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNN, MMWide>(a, s);
     case 3: return mm_launch<T, kModeNN, MMSmall>(a, s);
-    default: return mm_launch<T, kModeNN, MMLong>(a, s);
+    case 4: return mm_launch<T, kModeNN, MMLong>(a, s);
+    default: return mm_launch<T, kModeNN, MMDeep>(a, s);
   }
 }
 

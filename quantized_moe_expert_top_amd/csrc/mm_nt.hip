@@ -30,7 +30,8 @@ hipError_t launch(const MMArgs& a, hipStream_t s) {
     case 1: return mm_launch<T, kModeNT, MMMid>(a, s);
     case 2: return mm_launch<T, kModeNT, MMWide>(a, s);
     case 3: return mm_launch<T, kModeNT, MMSmall>(a, s);
-    default: return mm_launch<T, kModeNT, MMLong>(a, s);
+    case 4: return mm_launch<T, kModeNT, MMLong>(a, s);
+    default: return mm_launch<T, kModeNT, MMDeep>(a, s);
   }
 }
 

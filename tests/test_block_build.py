@@ -45,7 +45,7 @@ def stray_waits(text, kernel):
     return found
 
 
-@pytest.mark.parametrize("source,kernels", [("mm_nt.hip", 10), ("mm_nn.hip", 10)])
+@pytest.mark.parametrize("source,kernels", [("mm_nt.hip", 12), ("mm_nn.hip", 12)])
 def test_no_waits_but_the_counted_ones(source, kernels):
     found = stray_waits(assembly(source), "mm_kernel")
     assert len(found) == kernels, sorted(found)

@@ -876,6 +876,8 @@ GEOMETRIES = [
     # few results of long contractions: cut in parts, or over a block's waves
     (3, 464, 4704, 0), (946, 256, 5712, 0), (30, 2048, 4112, 0), (401, 5624, 128, 0),
     (70, 96, 2000, 0), (3698, 104, 1152, 0), (200, 2952, 112, 0),
+    # one deep block per CU
+    (1219, 2056, 1736, 0), (347, 6000, 3872, 0), (320, 1696, 8432, 0),
     # rows of dw that are no whole cache lines, more than the caches hold
     (25, 232, 3552, 53),
 ]
