@@ -9,7 +9,7 @@
 // partial tiles are added in LDS in wave order, so the result does not depend
 // on timing.
 #pragma once
-#include "mm.h"
+#include "mm_launch.h"
 
 namespace moe {
 
@@ -162,12 +162,17 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
   }
 }
 
-// us of a dense product: blocks of 16 MT rows x 16 columns, `step` per 64 k for the
-// first 256 of them and a fifth more for each further 256 (401 x 288 x 2952: 16 rows
-// 10.8 us timed, 11.0 here; 32 rows 8.9, 9.0; 64 x 64 tiles 12.4).
-inline double mm_few_cost(int mt, int rows, int ndim, int kdim) {
-  const double blocks = static_cast<double>((rows + 16 * mt - 1) / (16 * mt)) * ((ndim + 15) / 16);
-  const double step = mt == 1 ? 0.072 : 0.104, start = mt == 1 ? 3.4 : 4.2;
+// us of a product: blocks of 16 MT rows x 16 columns, `step` per 64 k for the first
+// 256 of them and a fifth more for each further 256 (401 x 288 x 2952: 16 rows 10.8
+// us timed, 11.0 here; 32 rows 8.9, 9.0; 64 x 64 tiles 12.4), half of it for rows
+// that are not there (16 rows of 16 experts x 688 x 1248 6.3, 7.0; 64 x 64 8.9).
+// Experts' tiles in more than 1024 blocks stream weights, which the larger tiles do
+// better (16 rows of 16 experts x 1536 x 2048: 20.2, 64 x 64 15.7).
+inline double mm_few_cost(int mt, int rows, int E, int ndim, int kdim) {
+  const double tiles = mm_row_tiles(16 * mt, rows, E), blocks = tiles * ((ndim + 15) / 16);
+  if (E != 0 && blocks > 1024) return 1e300;
+  const double fill = rows / (tiles * 16 * mt);
+  const double step = (mt == 1 ? 0.072 : 0.104) * (0.5 + 0.5 * fill), start = mt == 1 ? 3.4 : 4.2;
   const double rounds = __builtin_ceil(blocks / 256);
   return start + (kdim + 63) / 64 * step * (1.0 + 1.2 * (rounds - 1)) + 0.5 * (rounds - 1);
 }

@@ -9,22 +9,16 @@ namespace {
 template <class T>
 hipError_t launch(const MMArgs& a, hipStream_t s) {
   const int E = a.offsets ? a.E : 0;
-  const int act = E == 0 ? 1 : a.rows < E ? a.rows : E;   // experts in use, at most
   // Few rows, or few results of a long K: the kernel that splits K over a block's
   // waves. Measured at 2 x 4096 x 7168: 11.7 us against 23.2 (Small); 32 rows: 22.3
-  // against 23.5. With several experts in use the tiles fill the chip by themselves
-  // (16 rows of 14 experts x 1536 x 2048: 20.2 against 15.7, Wide), unless their
-  // tiles are few (2 rows of 2 experts x 4096 x 4096: 14.1 against 15.8, Small).
+  // against 23.5. Where several experts are in use the tiles mostly fill the chip by
+  // themselves.
   const MMPick pick = mm_pick_rows(a.rows, E, a.ndim, a.kdim, a.act);
-  if (E == 0) {
-    const double f1 = mm_few_cost(1, a.rows, a.ndim, a.kdim),
-                 f2 = mm_few_cost(2, a.rows, a.ndim, a.kdim);
-    if (a.rows <= 16 || f1 < pick.cost || f2 < pick.cost)
-      return a.rows <= 16 || f1 <= f2 ? mm_few_launch<T, 1, 8, 2>(a, s)
-                                      : mm_few_launch<T, 2, 8, 2>(a, s);
-  } else if (a.rows <= 4 * act && act * ((a.ndim + 127) / 128) <= 96) {
-    return mm_few_launch<T, 1, 8, 2>(a, s);
-  }
+  const double f1 = mm_few_cost(1, a.rows, E, a.ndim, a.kdim),
+               f2 = E == 0 ? mm_few_cost(2, a.rows, E, a.ndim, a.kdim) : 1e300;
+  if ((E == 0 && a.rows <= 16) || f1 < pick.cost || f2 < pick.cost)
+    return a.rows <= 16 || f1 <= f2 ? mm_few_launch<T, 1, 8, 2>(a, s)
+                                    : mm_few_launch<T, 2, 8, 2>(a, s);
   switch (pick.geom) {
     case 0: return mm_launch<T, kModeNT, MMBig>(a, s);
     case 1: return mm_launch<T, kModeNT, MMMid>(a, s);

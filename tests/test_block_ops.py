@@ -873,6 +873,7 @@ GEOMETRIES = [
     (8200, 4104, 7184, 0), (2500, 264, 4112, 0), (4093, 2048, 1536, 0), (1100, 96, 2048, 0),
     (40000, 72, 80, 0), (700, 2056, 1040, 0), (8200, 4104, 7184, 3), (4000, 2056, 1040, 6),
     (9000, 1032, 2064, 3), (300, 64, 2064, 40), (12000, 520, 2064, 3), (16000, 1032, 2064, 60),
+    (84, 3480, 288, 14), (123, 1976, 160, 66),
     # few results of long contractions: cut in parts, or over a block's waves
     (3, 464, 4704, 0), (946, 256, 5712, 0), (30, 2048, 4112, 0), (401, 5624, 128, 0),
     (70, 96, 2000, 0), (3698, 104, 1152, 0), (200, 2952, 112, 0),
