@@ -141,7 +141,8 @@ MOE_API moe_status moe_linear(const moe_mm_shape* shape, const void* x, const vo
  *   dbias  dw_dtype [N] or NULL
  * dz is rounded to dtype where it enters the products, not in dbias. With
  * rows = 0, dw and dbias are set to zero. `ws` must hold
- * moe_linear_backward_workspace(shape) bytes.
+ * moe_linear_backward_workspace(shape) bytes, which grow with rows: a workspace
+ * for the most rows serves fewer.
  */
 MOE_API size_t moe_linear_backward_workspace(const moe_mm_shape* shape);
 MOE_API moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy,

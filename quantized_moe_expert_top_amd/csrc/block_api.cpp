@@ -103,17 +103,11 @@ moe::MMArgs mm_args(const moe_mm_shape* s, const int32_t* offsets, const int32_t
   return a;
 }
 
-// Workspace of the gradients: dz, the bias sums' strips, the split products.
+// Workspace of the gradients: dz, the bias sums' strips, the split products. Grows
+// with the rows.
 struct MMWs {
   size_t dz, strips, parts, total;
 };
-size_t dx_parts(const moe_mm_shape* s, const moe::MMBackwardPlan& p) {
-  return p.nn_splits > 1 ? align256(static_cast<size_t>(s->rows) * p.nn_splits * s->K * 4) : 0;
-}
-size_t dw_parts(const moe_mm_shape* s, bool grouped, const moe::MMBackwardPlan& p) {
-  const int E = grouped ? s->E : 1;
-  return p.tn_splits > 1 ? align256(static_cast<size_t>(E) * p.tn_splits * s->N * s->K * 4) : 0;
-}
 MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   MMWs w = {};
   size_t at = 0;
@@ -121,10 +115,9 @@ MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   if (!grouped || s->act != MOE_ACT_NONE)
     at += align256(static_cast<size_t>(s->rows) * s->N * 2);
   w.strips = at;
-  if (!grouped) at += align256(static_cast<size_t>(moe::dz_strips(s->rows, s->N, s->act)) * s->N * 4);
+  if (!grouped) at += align256(static_cast<size_t>(moe::dz_most_strips(s->rows, s->N, s->act)) * s->N * 4);
   w.parts = at;
-  const moe::MMBackwardPlan p = moe::mm_backward_plan(s->rows, grouped ? s->E : 0, s->N, s->K);
-  w.total = at + dx_parts(s, p) + dw_parts(s, grouped, p);
+  w.total = at + moe::mm_backward_parts(s->rows, grouped ? s->E : 0, s->N, s->K);
   return w;
 }
 
@@ -157,7 +150,7 @@ moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* 
     tn.c_f32 = 1;
     sum_dw = {reinterpret_cast<const float*>(parts), tn.splits, tn.E,
               static_cast<long long>(s->N) * s->K, dw, dw_dtype};
-    parts += dw_parts(s, offsets != nullptr, plan);
+    parts += align256(static_cast<size_t>(tn.E) * tn.splits * s->N * s->K * 4);
   }
   if (dx && plan.nn_splits > 1) {
     nn.splits = plan.nn_splits;

@@ -199,9 +199,12 @@ __global__ __launch_bounds__(256) void sums_kernel(const SplitSum a, const Split
 // Rows of a strip: as many strips as fill the chip (about 768 blocks of 512
 // columns: 4093 x 1536 9 us, 23 us with 192 blocks), and no more, since their sums
 // are read again.
-int strip_rows_of(int rows, int No) {
+int most_strips(int No) {
   const int cb = (No + kDzCols - 1) / kDzCols;
-  const int strips = cb >= 768 ? 1 : 768 / cb;
+  return cb >= 768 ? 1 : 768 / cb;
+}
+int strip_rows_of(int rows, int No) {
+  const int strips = most_strips(No);
   const int r = static_cast<int>((static_cast<long long>(rows) + strips - 1) / strips);
   return r < 8 ? 8 : (r + 3) / 4 * 4;
 }
@@ -211,6 +214,12 @@ int strip_rows_of(int rows, int No) {
 int dz_strips(int rows, int N, int act) {
   const int sr = strip_rows_of(rows, act == kActSwiglu ? N / 2 : N);
   return static_cast<int>((static_cast<long long>(rows) + sr - 1) / sr);
+}
+
+int dz_most_strips(int rows, int N, int act) {
+  const int s = most_strips(act == kActSwiglu ? N / 2 : N);
+  const int all = static_cast<int>((static_cast<long long>(rows) + 7) / 8);
+  return all < s ? all : s;
 }
 
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,

@@ -27,6 +27,7 @@ struct MMBackwardPlan {
   int pair, nn, nn_splits, tn, tn_splits;
 };
 MMBackwardPlan mm_backward_plan(int rows, int E, int N, int K);   // E 0: no experts
+size_t mm_backward_parts(int rows, int E, int N, int K);   // bytes for all parts of up to `rows` rows
 // Both gradients, and a sum, in one launch.
 hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
                           bool fp16, hipStream_t s);
@@ -35,6 +36,7 @@ hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum
 // (part [dz_strips(rows, N, act)][N], may be NULL). offsets NULL: all rows; otherwise
 // rows [offsets[0], offsets[E]).
 int dz_strips(int rows, int N, int act);
+int dz_most_strips(int rows, int N, int act);   // of up to `rows` rows
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
                      int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s);
 // out[e][i] = sum over the parts of part[e][s][i], in order; n values per e (a

@@ -71,17 +71,17 @@ static MMBackwardPlan plan_of(int rows, int E, int N, int K) {
         best = {0, nn[i].geom, nn[i].splits, tn[j].geom, tn[j].splits};
       }
     }
-  double tn_stages = static_cast<double>(rows) / groups / 64 + (grouped ? 0.5 : 0.0);
-  if (tn_stages < 1.0) tn_stages = 1.0;
-  const double nn_stages = (N + 63) / 64;
+  const double tn_stages = mm_tn_stages(rows, groups), nn_stages = (N + 63) / 64;
+  const int most_dx = grouped ? 1 : mm_most_dx_splits(rows, N, K),
+            most_dw = grouped ? 1 : mm_most_dw_splits(rows, 1, N, K);
   const MMCost* const table[2] = {&kMMMidCost, &kMMSmallCost};
   for (int i = 0; i < 2; ++i) {
     const MMCost& c = *table[i];
     const double kt = (K + c.bn - 1) / c.bn;
     const double tn_tiles = groups * static_cast<double>((N + c.bm - 1) / c.bm) * kt,
                  nn_tiles = mm_row_tiles(c.bm, rows, E) * kt;
-    for (int a = 1; a == 1 || (!grouped && a <= 32 && nn_stages >= 4.0 * a); a *= 2)
-      for (int b = 1; b == 1 || (!grouped && b <= 32 && tn_stages >= 4.0 * b); b *= 2) {
+    for (int a = 1; a <= most_dx; a *= 2)
+      for (int b = 1; b <= most_dw; b *= 2) {
         const double cost = pair_cost(c, tn_tiles * b, tn_stages / b, nn_tiles * a, nn_stages / a) +
                             mm_split_cost(static_cast<double>(rows) * K, a) +
                             mm_split_cost(static_cast<double>(N) * K, b) +
@@ -110,6 +110,18 @@ MMBackwardPlan mm_backward_plan(int rows, int E, int N, int K) {
   if (!k.set || k.rows != rows || k.E != E || k.N != N || k.K != K)
     k = {true, rows, E, N, K, plan_of(rows, E, N, K)};
   return k.plan;
+}
+
+size_t mm_backward_parts(int rows, int E, int N, int K) {
+  const int groups = E > 0 ? E : 1, dw = mm_most_dw_splits(rows, groups, N, K);
+  size_t n = dw > 1 ? (static_cast<size_t>(groups) * dw * N * K * 4 + 255) & ~size_t{255} : 0;
+  if (E == 0) {
+    // for every count of rows up to this one
+    const size_t most = mm_most_splits((N + 63) / 64, 1), all = most * rows * K * 4,
+                 cap = static_cast<size_t>(kMMSplitTiles) * 64 * 64 * 4;
+    if (most > 1) n += ((all < cap ? all : cap) + 255) & ~size_t{255};
+  }
+  return n;
 }
 
 hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,

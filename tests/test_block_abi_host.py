@@ -371,6 +371,28 @@ def test_binding_raises_library_errors():
     assert ei.value.status == EINVAL
 
 
+def test_workspaces_grow_with_rows():
+    """A workspace for the most rows serves any fewer."""
+    import quantized_moe_expert_top_amd as moe
+    g = torch.Generator().manual_seed(3)
+
+    def rnd(lo, hi, step):
+        v = lo * (hi / lo) ** torch.rand(1, generator=g).item()
+        return max(step, int(v) // step * step)
+
+    ladder = sorted({rnd(1, 40000, 1) for _ in range(150)} | set(range(0, 140)) | {4093, 8192, 8193})
+    for _ in range(60):
+        K, N, E = rnd(8, 9000, 8), rnd(16, 9000, 16), rnd(1, 256, 1)
+        for act in ("none", "swiglu"):
+            lin = [moe.linear_backward_workspace(r, K, N, act) for r in ladder]
+            grp = [moe.grouped_mm_backward_workspace(r, K, N, E, act) for r in ladder]
+            assert lin == sorted(lin), (K, N, act)
+            assert grp == sorted(grp), (K, N, E, act)
+    for H in (8, 512, 520, 2048, 16384):
+        n = [moe.block_norm_backward_workspace(r, H) for r in ladder]
+        assert n == sorted(n), H
+
+
 def test_workspace_queries():
     import quantized_moe_expert_top_amd as moe
     assert moe.grouped_mm_backward_workspace(0, 64, 32, 4, "swiglu") == 0

@@ -149,6 +149,27 @@ def test_linear_backward_single_outputs(which):
     assert torch.equal(one, every[which])
 
 
+def test_backward_in_a_workspace_for_more_rows():
+    """A workspace sized for the most rows serves fewer, cut contractions included."""
+    import quantized_moe_expert_top_amd as moe
+    K, N = 264, 4112
+    need = moe.linear_backward_workspace(3000, K, N, "silu")
+    big = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for rows in (3000, 946, 130, 3, 1):
+        mk = Maker(rows)
+        x, w, z, dy = mk((rows, K), BF), mk((N, K), BF), mk((rows, N), BF), mk((rows, N), BF)
+        outs = []
+        for ws in (big[:need], workspace(moe.linear_backward_workspace(rows, K, N, "silu"))):
+            dx, dw, db = (torch.full(s, float("nan"), dtype=BF, device="cuda")
+                          for s in ((rows, K), (N, K), (N,)))
+            moe.linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, act="silu", z=z, ws=ws)
+            outs.append((dx, dw, db))
+        torch.cuda.synchronize()
+        for a, b in zip(*outs):
+            assert torch.isfinite(a).all() and torch.equal(a, b), rows
+        assert (big[need:] == 0xA5).all()
+
+
 def test_linear_adds_in_place():
     import quantized_moe_expert_top_amd as moe
     for rows, K, N in ((2, 264, 48), (140, 72, 272)):
