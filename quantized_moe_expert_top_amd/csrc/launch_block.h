@@ -27,7 +27,8 @@ struct MMBackwardPlan {
   int pair, nn, nn_splits, tn, tn_splits;
 };
 MMBackwardPlan mm_backward_plan(int rows, int E, int N, int K);   // E 0: no experts
-size_t mm_backward_parts(int rows, int E, int N, int K);   // bytes for all parts of up to `rows` rows
+// bytes for all parts of up to `rows` rows
+size_t mm_backward_parts(int rows, int E, int N, int K);
 // Both gradients, and a sum, in one launch.
 hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
                           bool fp16, hipStream_t s);
