@@ -16,7 +16,7 @@ using MMSmall = MMGeom<64, 64, 2, 2, 64, 4, 2>;    // 4 waves, two blocks per CU
 // so a long K goes to Big (8192 x 4096 x 7168: 447 us expected against 376); with
 // few stages it wins (128 experts, 32768 rows x 2048 x 768 to float32: 215 against
 // 240 us; its row gradient 150 against 167).
-using MMLong = MMGeom<128, 256, 2, 2, 32, 3, 2>;
+using MMLong = MMGeom<128, 256, 1, 4, 32, 3, 2>;
 // 8 waves, one block per CU, four stages: where a dense product has too few tiles
 // for two blocks per CU a block alone has to keep enough loads in flight (1219 x 1728
 // x 5120: 40 us, Mid 60, Wide 50; 5549 x 384 x 5760: 40, Mid 63, Wide 53).
