@@ -15,7 +15,8 @@ using MMSmall = MMGeom<64, 64, 2, 2, 64, 4, 2>;    // 4 waves, two blocks per CU
 // other's multiplies. Its 32-k stages read half cache lines of a K-major operand,
 // so a long K goes to Big (8192 x 4096 x 7168: 447 us expected against 376); with
 // few stages it wins (128 experts, 32768 rows x 2048 x 768 to float32: 215 against
-// 240 us; its row gradient 150 against 167).
+// 240 us; its row gradient 150 against 167). Waves of 128 x 64 (of 64 x 128: 223
+// against 217, row gradients of 1536 columns 283 against 277).
 using MMLong = MMGeom<128, 256, 1, 4, 32, 3, 2>;
 // 8 waves, one block per CU, four stages: where a dense product has too few tiles
 // for two blocks per CU a block alone has to keep enough loads in flight (1219 x 1728
