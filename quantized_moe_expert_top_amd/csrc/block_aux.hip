@@ -69,11 +69,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, in
         load8<T>(z, r * N + col, false, g);
         load8<T>(z, r * N + No + col, false, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float sg = sigmoid_f32(g[i]);
-          du[i] = d[i] * g[i] * sg;
-          d[i] = d[i] * u[i] * (sg * (1.0f + g[i] * (1.0f - sg)));
-        }
+        for (int i = 0; i < 8; ++i) swiglu_grad_f32(d[i], g[i], u[i], d[i], du[i]);
         if (dz) {
           store8<T>(dz, r * N + col, d);
           store8<T>(dz, r * N + No + col, du);
@@ -143,11 +139,7 @@ __global__ __launch_bounds__(256) void dz_flat_kernel(const void* __restrict__ d
       load8<T>(z, r * N + col, false, g);
       load8<T>(z, r * N + No + col, false, u);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float sg = sigmoid_f32(g[x]);
-        du[x] = d[x] * g[x] * sg;
-        d[x] = d[x] * u[x] * (sg * (1.0f + g[x] * (1.0f - sg)));
-      }
+      for (int x = 0; x < 8; ++x) swiglu_grad_f32(d[x], g[x], u[x], d[x], du[x]);
       store8<T>(dz, r * N + col, d);
       store8<T>(dz, r * N + No + col, du);
     } else {

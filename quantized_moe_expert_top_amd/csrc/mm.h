@@ -123,6 +123,14 @@ __device__ __forceinline__ float act_grad_f32(float z, int act) {
   return 1.0f;
 }
 
+// Gradients of y = silu(g) u in g and u. dy multiplies last: dy g or dy u may leave
+// float32's range (and infinity times silu = 0 be NaN) where the gradient does not.
+__device__ __forceinline__ void swiglu_grad_f32(float dy, float g, float u, float& dg, float& du) {
+  const float s = sigmoid_f32(g);
+  du = dy * (g * s);
+  dg = dy * (u * (s * (1.0f + g * (1.0f - s))));
+}
+
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
 __device__ __forceinline__ void mm_area8(const float* p, float (&v)[8]) {
   const f32x4_t a = reinterpret_cast<const f32x4_t*>(p)[0], b = reinterpret_cast<const f32x4_t*>(p)[1];
