@@ -265,7 +265,7 @@ moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy, co
   if (shape->act != MOE_ACT_NONE) {
     void* out = base + need.dz;
     st = launched(moe::launch_dz(dy, false, z, expert_offsets, shape->E, shape->rows, shape->N,
-                                 shape->act, shape->dtype == MOE_FP16, out, nullptr, s),
+                                 shape->act, shape->dtype == MOE_FP16, out, nullptr, false, s),
                   "activation gradient launch");
     if (st) return st;
     dz = out;
@@ -364,7 +364,7 @@ moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_
   if (want_dz || dbias) {
     st = launched(moe::launch_dz(dy, dy_dtype == MOE_F32, z, nullptr, 1, shape->rows, shape->N,
                                  shape->act, shape->dtype == MOE_FP16,
-                                 want_dz ? base + need.dz : nullptr, strips, s),
+                                 want_dz ? base + need.dz : nullptr, strips, dw_dtype == MOE_F32, s),
                   "activation gradient launch");
     if (st) return st;
   }

@@ -31,10 +31,11 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float (&v)[8]) 
 
 // A block takes 512 columns of dy (8 per thread) and a strip of rows, four at a
 // time; bound by the bytes of dy, z and dz. The column sums stay in registers
-// over the strip and are joined in LDS in a fixed order.
+// over the strip and are joined in LDS in a fixed order. EXACT (see mm.h): where the
+// bias gradient is float32.
 constexpr int kDzCols = 512;
 
-template <class T, bool SWIGLU>
+template <class T, bool SWIGLU, bool EXACT>
 __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, int dy_f32,
                                                  const void* __restrict__ z,
                                                  const int* __restrict__ offsets, int E, int rows,
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, in
         load8<T>(z, r * N + col, false, g);
         load8<T>(z, r * N + No + col, false, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) swiglu_grad_f32(d[i], g[i], u[i], d[i], du[i]);
+        for (int i = 0; i < 8; ++i) swiglu_grad_f32<EXACT>(d[i], g[i], u[i], d[i], du[i]);
         if (dz) {
           store8<T>(dz, r * N + col, d);
           store8<T>(dz, r * N + No + col, du);
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, in
         if (act != 0) {
           load8<T>(z, r * N + col, false, g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] *= act_grad_f32(g[i], act);
+          for (int i = 0; i < 8; ++i) d[i] *= act_grad_f32<EXACT>(g[i], act);
         }
         if (dz) store8<T>(dz, r * N + col, d);
       }
@@ -139,14 +140,14 @@ __global__ __launch_bounds__(256) void dz_flat_kernel(const void* __restrict__ d
       load8<T>(z, r * N + col, false, g);
       load8<T>(z, r * N + No + col, false, u);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) swiglu_grad_f32(d[x], g[x], u[x], d[x], du[x]);
+      for (int x = 0; x < 8; ++x) swiglu_grad_f32<false>(d[x], g[x], u[x], d[x], du[x]);
       store8<T>(dz, r * N + col, d);
       store8<T>(dz, r * N + No + col, du);
     } else {
       if (act != 0) {
         load8<T>(z, r * N + col, false, g);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) d[x] *= act_grad_f32(g[x], act);
+        for (int x = 0; x < 8; ++x) d[x] *= act_grad_f32<false>(g[x], act);
       }
       store8<T>(dz, r * N + col, d);
     }
@@ -215,7 +216,8 @@ int dz_most_strips(int rows, int N, int act) {
 }
 
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
-                     int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s) {
+                     int rows, int N, int act, bool fp16, void* dz, float* part, bool part_f32,
+                     hipStream_t s) {
   if (rows == 0) return hipSuccess;
   const int No = act == kActSwiglu ? N / 2 : N;
   const int cb = (No + kDzCols - 1) / kDzCols;
@@ -234,13 +236,22 @@ hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offs
     }
     return hipGetLastError();
   }
-  if (act == kActSwiglu) {
-    if (fp16) dz_kernel<fp16_tag, true><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
-    else dz_kernel<bf16_tag, true><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
-  } else {
-    if (fp16) dz_kernel<fp16_tag, false><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
-    else dz_kernel<bf16_tag, false><<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
-  }
+  auto run = [&](auto tag, auto swiglu, auto exact) {
+    dz_kernel<decltype(tag), decltype(swiglu)::value, decltype(exact)::value>
+        <<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
+  };
+  auto typed = [&](auto tag) {
+    if (act == kActSwiglu) {
+      if (part_f32) run(tag, std::true_type{}, std::true_type{});
+      else run(tag, std::true_type{}, std::false_type{});
+    } else if (part_f32 && act != 0) {
+      run(tag, std::false_type{}, std::true_type{});
+    } else {
+      run(tag, std::false_type{}, std::false_type{});
+    }
+  };
+  if (fp16) typed(fp16_tag{});
+  else typed(bf16_tag{});
   return hipGetLastError();
 }
 

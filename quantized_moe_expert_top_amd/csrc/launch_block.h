@@ -35,11 +35,12 @@ hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum
 
 // dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
 // (part [dz_strips(rows, N, act)][N], may be NULL). offsets NULL: all rows; otherwise
-// rows [offsets[0], offsets[E]).
+// rows [offsets[0], offsets[E]). part_f32: the sums' result is float32.
 int dz_strips(int rows, int N, int act);
 int dz_most_strips(int rows, int N, int act);   // of up to `rows` rows
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
-                     int rows, int N, int act, bool fp16, void* dz, float* part, hipStream_t s);
+                     int rows, int N, int act, bool fp16, void* dz, float* part, bool part_f32,
+                     hipStream_t s);
 // out[e][i] = sum over the parts of part[e][s][i], in order; n values per e (a
 // multiple of 4). out NULL: none.
 struct SplitSum {

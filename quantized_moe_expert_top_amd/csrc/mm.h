@@ -74,61 +74,103 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
   }
 }
 
-// Activations and their derivatives in float32. The exponential and reciprocal
-// are the hardware's (about 1 ulp); silu(z) for z below about -88 is -0 through
-// a zero reciprocal.
-__device__ __forceinline__ float sigmoid_f32(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
+// Activations and their derivatives in float32. `u` below is 2^-24; the hardware's
+// exp2 and reciprocal are within 2 u. EXACT, for results that are stored as float32:
+// within 18 u of the value itself over the whole range. Otherwise the exponential is
+// one exp2, whose argument's rounding makes e^x off by |x| u: up to 2^-17 of a result
+// in an activation's far tail, which the rounding to 16 bits (2^-12 or 2^-9) hides.
+// 8192 x 4096 x 1024 to bf16: silu 82 us, gelu 93, SwiGLU 69; 88, 98 and 72 EXACT.
+// Results whose exponential is below 2^-126 become 0 (|silu| < 1.1e-36).
+//
+// EXACT: exp(x + lo), x <= 0, |lo| small, within 3.2 u: exp2(t), t = x log2 e rounded,
+// times 1 + d with d = x - t ln 2 + lo, what t's rounding left out. Held at -104,
+// where the result is 0, so that an infinite x gives no infinity minus infinity.
+__device__ __forceinline__ float exp_neg_f32(float x, float lo = 0.0f) {
+  x = __builtin_fmaxf(x, -104.0f);
+  const float t = x * 1.4426950408889634f;
+  float d = __builtin_fmaf(t, -0.693147182464599609375f, x);   // ln 2 to 24 bits,
+  d = __builtin_fmaf(t, 1.904654323148236e-9f, d) + lo;        // and the rest of it
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, d, e);
+}
+// s = 1 / (1 + e^-z) and c = 1 - s. EXACT: both through e^-|z|, so that neither
+// overflows and neither is a difference; each within 7.2 u.
+template <bool EXACT>
+__device__ __forceinline__ void sigmoid2_f32(float z, float& s, float& c) {
+  if constexpr (EXACT) {
+    const float e = exp_neg_f32(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+    s = z < 0.0f ? er : r;
+    c = z < 0.0f ? r : er;
+  } else {
+    s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
+    c = 1.0f - s;
+  }
+}
+template <bool EXACT>
+__device__ __forceinline__ float silu_f32(float z) {
+  float s, c;
+  sigmoid2_f32<EXACT>(z, s, c);
+  return z * s;
 }
 // The Gaussian cdf, and e = exp(-z^2 / 2): with s = |z| the tail is
 // cdf(-s) = erfc(s / sqrt 2) / 2 = e t P(t), t = 1 / (1 + 0.325 s), P of degree 9 by
-// least relative error (5e-8 exactly, 3.5e-7 in float32); relative to the tail, so
-// nothing cancels for negative z. About 20 instructions; the library's erfc is
-// exact to an ulp in some hundred (8192 x 4096 gelu outputs: 157 us of product with
-// it).
+// least relative error (1.4 u); relative to the tail, so nothing cancels for
+// negative z. EXACT: s^2 goes into the exponential with its rounding error; within
+// 17 u in all (t's 3 u count 2.5 times through t P, Horner's steps 2.9 u, e 3.2 u).
+// The library's erfc takes some hundred instructions (8192 x 4096 x 1024 with it:
+// 157 us).
+template <bool EXACT>
 __device__ __forceinline__ float normal_cdf_f32(float z, float& e) {
-  const float s = __builtin_fabsf(z), t = __builtin_amdgcn_rcpf(1.0f + 0.325f * s);
-  e = __builtin_amdgcn_exp2f(-0.72134752044448170f * s * s);
+  float s = __builtin_fabsf(z);
+  if constexpr (EXACT) s = __builtin_fminf(s, 16.0f);   // e is 0 from there on
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.325f, s, 1.0f)), q = s * s;
+  if constexpr (EXACT) e = exp_neg_f32(-0.5f * q, -0.5f * __builtin_fmaf(s, s, -q));
+  else e = __builtin_amdgcn_exp2f(-0.72134752044448170f * q);
   float p = -0.0211383961f;
-  p = p * t + 0.091305308f;
-  p = p * t - 0.129665121f;
-  p = p * t + 0.0433723368f;
-  p = p * t - 0.00181293103f;
-  p = p * t + 0.0542199835f;
-  p = p * t + 0.0884514824f;
-  p = p * t + 0.115954153f;
-  p = p * t + 0.129656926f;
-  p = p * t + 0.12965624f;
+  p = __builtin_fmaf(p, t, 0.091305308f);
+  p = __builtin_fmaf(p, t, -0.129665121f);
+  p = __builtin_fmaf(p, t, 0.0433723368f);
+  p = __builtin_fmaf(p, t, -0.00181293103f);
+  p = __builtin_fmaf(p, t, 0.0542199835f);
+  p = __builtin_fmaf(p, t, 0.0884514824f);
+  p = __builtin_fmaf(p, t, 0.115954153f);
+  p = __builtin_fmaf(p, t, 0.129656926f);
+  p = __builtin_fmaf(p, t, 0.12965624f);
   const float tail = p * t * e;
   return z >= 0.0f ? 1.0f - tail : tail;
 }
+template <bool EXACT>
 __device__ __forceinline__ float act_f32(float z, int act) {
   if (act == 1) return z > 0.0f ? z : (z != z ? z : 0.0f);   // relu; NaN stays
-  if (act == 2) return z * sigmoid_f32(z);
+  if (act == 2) return silu_f32<EXACT>(z);
   float e;
-  if (act == 3) return z * normal_cdf_f32(z, e);   // gelu
+  if (act == 3) return z * normal_cdf_f32<EXACT>(z, e);   // gelu
   return z;
 }
+template <bool EXACT>
 __device__ __forceinline__ float act_grad_f32(float z, int act) {
   if (act == 1) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if (act == 2) {
-    const float s = sigmoid_f32(z);
-    return s * (1.0f + z * (1.0f - s));
+    float s, c;
+    sigmoid2_f32<EXACT>(z, s, c);
+    return s * __builtin_fmaf(z, c, 1.0f);
   }
   if (act == 3) {   // cdf + z pdf
     float e;
-    const float cdf = normal_cdf_f32(z, e);
-    return cdf + z * 0.39894228040143268f * e;
+    const float cdf = normal_cdf_f32<EXACT>(z, e);
+    return __builtin_fmaf(z * 0.39894228040143268f, e, cdf);
   }
   return 1.0f;
 }
 
 // Gradients of y = silu(g) u in g and u. dy multiplies last: dy g or dy u may leave
 // float32's range (and infinity times silu = 0 be NaN) where the gradient does not.
+template <bool EXACT>
 __device__ __forceinline__ void swiglu_grad_f32(float dy, float g, float u, float& dg, float& du) {
-  const float s = sigmoid_f32(g);
+  float s, c;
+  sigmoid2_f32<EXACT>(g, s, c);
   du = dy * (g * s);
-  dg = dy * (u * (s * (1.0f + g * (1.0f - s))));
+  dg = dy * (u * (s * __builtin_fmaf(g, c, 1.0f)));
 }
 
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
@@ -782,11 +824,19 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
           mm_area8(area + r * kRowF + CW / 2 + c, u);
           if (ADDED && a.bias) mm_add8<T>(add.bias_up, u);
           if (a.z) mm_put16(mm_pack8<T>(u), z_rs, zoff + half_n * 2, stream);
+          auto gated = [&](auto exact) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) v[t] = act_f32(v[t], 2) * u[t];
+            for (int t = 0; t < 8; ++t) v[t] = silu_f32<decltype(exact)::value>(v[t]) * u[t];
+          };
+          if (a.c_f32) gated(std::true_type{});
+          else gated(std::false_type{});
         } else if (a.act != 0) {
+          auto activated = [&](auto exact) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) v[t] = act_f32(v[t], a.act);
+            for (int t = 0; t < 8; ++t) v[t] = act_f32<decltype(exact)::value>(v[t], a.act);
+          };
+          if (a.c_f32) activated(std::true_type{});
+          else activated(std::false_type{});
         }
       }
       if (MODE == kModeNT && ADDED && a.residual) {

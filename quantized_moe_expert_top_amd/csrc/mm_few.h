@@ -144,9 +144,9 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
         g += lo;
       }
       if (z) z[p * a.ndim + half_n + col] = static_cast<uint16_t>(pack2<T>(g, 0.0f));
-      v = act_f32(v, 2) * g;
+      v = (a.c_f32 ? silu_f32<true>(v) : silu_f32<false>(v)) * g;
     } else {
-      v = act_f32(v, a.act);
+      v = a.c_f32 ? act_f32<true>(v, a.act) : act_f32<false>(v, a.act);
     }
     const size_t at = p * out_w + col;
     if (a.residual) {

@@ -66,3 +66,116 @@ def test_swiglu_gradient_of_large_operands(grouped, dbias):
             continue
         assert torch.isfinite(got).all(), f"{name}: non-finite values"
         assert ((got.double() - ref).abs() <= tol * ref.abs()).all(), name
+
+
+# Error bounds in units of u = 2^-24, half a step of float32; the hardware's exp2 and
+# reciprocal are within one step, 2 u.
+#   e^-a    exp2 2, the correction's fma 1, the argument's own rest 0.2         3.2
+#   sigmoid e^-|z| 3.2, 1 + e 1, reciprocal 2, product 1                        7.2
+#   silu    sigmoid 7.2, product 1                                              8.2
+#   silu'   = s (1 + z c): s 7.2, fma 1, product 1 on the value; c 7.2 on s |z| c
+#   cdf     fit 1.4, t (argument 1, reciprocal 2) times the 2.46 by which t P(t)
+#           moves with t, Horner's fused steps 2.9, two products 2, e 3.2      16.9
+#   gelu    cdf 16.9, product 1                                                17.9
+#   gelu'   cdf 16.9 on cdf; e 3.2, constant 1, product 1 on |z| pdf; fma 1
+U = 2.0 ** -24
+
+
+def silu64(z):
+    return z / (1 + torch.exp(-z))
+
+
+def silu_grad64(z):
+    s, c = 1 / (1 + torch.exp(-z)), 1 / (1 + torch.exp(z))
+    return s * (1 + z * c), U * (9.2 * (s * (1 + z * c)).abs() + 7.2 * s * z.abs() * c)
+
+
+def cdf64(z):
+    return 0.5 * torch.special.erfc(-z * 0.5 ** 0.5)
+
+
+def gelu_grad64(z):
+    cdf, pdf = cdf64(z), torch.exp(-z * z / 2) * (2 * torch.pi) ** -0.5
+    v = cdf + z * pdf
+    return v, U * (16.9 * cdf + 5.2 * z.abs() * pdf + v.abs())
+
+
+def arguments(lowest, highest, n):
+    """Both tails, the middle, and both sides of zero down to 1e-6."""
+    g = torch.Generator().manual_seed(11)
+    even = lowest + (highest - lowest) * torch.rand(n // 2, generator=g, dtype=torch.float64)
+    small = 10 ** (torch.rand(n - n // 2, generator=g, dtype=torch.float64) * 6.5 - 6)
+    small *= torch.randint(0, 2, small.shape, generator=g) * 2 - 1
+    m, e = torch.frexp(torch.cat((even, small.clamp(lowest, highest))))
+    return torch.ldexp((m * 2.0 ** 16).trunc(), e - 16)     # 16 bits: the sum of two operands
+
+
+RANGE = {"silu": (-87.0, 87.0), "gelu": (-13.0, 13.0), "swiglu": (-87.0, 87.0)}
+
+
+@pytest.mark.parametrize("rows", [1, 300])          # weights to registers, or tiles
+@pytest.mark.parametrize("t", [BF, HF])
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+def test_activation_error_is_relative_to_the_result(act, t, rows):
+    import quantized_moe_expert_top_amd as moe
+    No, K = 4096, 8
+    _say("activation", act, t, rows)
+    z = arguments(*RANGE[act], No).cuda()
+    hi = z.to(t)
+    lo = (z - hi.double()).to(t)
+    N = 2 * No if act == "swiglu" else No
+    w = torch.zeros((N, K), dtype=t, device="cuda")
+    w[:No, 0], w[:No, 1] = hi, lo
+    u = torch.ones(No, dtype=torch.float64, device="cuda")
+    if act == "swiglu":
+        g = torch.Generator(device="cuda")
+        g.manual_seed(4)
+        w[No:, 0] = torch.randn(No, generator=g, device="cuda").to(t)
+        u = w[No:, 0].double()
+    x = torch.zeros((rows, K), dtype=t, device="cuda")
+    x[:, :2] = 1
+    y = torch.empty((rows, No), dtype=F32, device="cuda")
+    moe.linear(x, w, y, act=act)
+    torch.cuda.synchronize()
+    z = hi.double() + lo.double()
+    assert torch.equal(z, z.float().double())         # exact in the product's float32
+    want = (z * cdf64(z) if act == "gelu" else silu64(z) * u)
+    tol = U * {"silu": 8.2, "gelu": 17.9, "swiglu": 9.2}[act] * want.abs() + 2.0 ** -149
+    err = ((y.double() - want).abs() / tol).max().item()
+    assert err <= 1.0, f"error {err:.3g} times its bound"
+
+
+@pytest.mark.parametrize("t", [BF, HF])
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+def test_gradient_error_is_relative_to_the_result(act, t):
+    """One row: its bias gradient in float32 is dz before it is rounded."""
+    import quantized_moe_expert_top_amd as moe
+    No, K = 4096, 8
+    N = 2 * No if act == "swiglu" else No
+    _say("gradient", act, t)
+    z = torch.ones((1, N), dtype=t, device="cuda")
+    z[0, :No] = arguments(*RANGE[act], No).to(t).clamp(*RANGE[act])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    if act == "swiglu":
+        z[0, No:] = torch.randn(No, generator=g, device="cuda").to(t)
+    dy = torch.randn((1, No), generator=g, device="cuda")
+    x = torch.zeros((1, K), dtype=t, device="cuda")
+    w = torch.zeros((N, K), dtype=t, device="cuda")
+    db = torch.empty((N,), dtype=F32, device="cuda")
+    ws = torch.empty(moe.linear_backward_workspace(1, K, N, act), dtype=torch.uint8, device="cuda")
+    moe.linear_backward(dy, x, w, dbias=db, act=act, z=z, ws=ws)
+    torch.cuda.synchronize()
+    d, v = dy[0].double(), z[0, :No].double()
+    if act == "gelu":
+        a, e = gelu_grad64(v)
+        want, tol = d * a, d.abs() * (e + U * a.abs())
+    else:
+        a, e = silu_grad64(v)
+        want, tol = d * a, d.abs() * (e + U * a.abs())
+        if act == "swiglu":
+            u, s = z[0, No:].double(), silu64(v)
+            want = torch.cat((want * u, d * s))
+            tol = torch.cat(((tol + U * (d * a).abs()) * u.abs(), 9.2 * U * (d * s).abs()))
+    err = ((db.double() - want).abs() / (tol + 2.0 ** -149)).max().item()
+    assert err <= 1.0, f"error {err:.3g} times its bound"
