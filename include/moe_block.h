@@ -53,7 +53,8 @@ extern "C" {
  * Shape of a product. Let No = N/2 for MOE_ACT_SWIGLU and N otherwise.
  *   rows    rows of y (grouped: the capacity R of the grouped arrays), at most
  *           2^31 - 2^16; rows*max(N, K) <= 2^38, and a launch holds fewer than
- *           2^32 threads (64 rows x 64 columns take 256)
+ *           2^32 threads (64 rows x 64 columns take 256; MOE_ESHAPE otherwise,
+ *           before any launch of the call)
  *   K, N    multiples of 8 (N of 16 for SWIGLU), N*K <= 2^30
  *   E       experts (1 .. MOE_MAX_EXPERTS); moe_linear* ignore it
  *   x_rows  rows of x when sorted_slot is given (x_rows*K <= 2^30); otherwise

@@ -103,6 +103,21 @@ moe::MMArgs mm_args(const moe_mm_shape* s, const int32_t* offsets, const int32_t
   return a;
 }
 
+// The sizes' last check, before anything is enqueued: what a launch's check returned.
+moe_status too_large(hipError_t check) {
+  if (check == hipSuccess) return MOE_OK;
+  return fail(MOE_ESHAPE, "a launch of these sizes would hold 2^32 threads or more");
+}
+
+moe_status run_forward(const moe::MMArgs& a, const moe_mm_shape* s, void* stream, const char* what) {
+  const int plan = moe::mm_forward_plan(s->rows, a.offsets ? s->E : 0, s->N, s->K, s->act);
+  const bool fp16 = s->dtype == MOE_FP16;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  moe_status r = too_large(moe::launch_mm_nt(a, plan, fp16, st, true));
+  if (r || (r = check_device()) != MOE_OK) return r;
+  return launched(moe::launch_mm_nt(a, plan, fp16, st, false), what);
+}
+
 // Workspace of the gradients: dz, the bias sums' strips, the split products. Grows
 // with the rows.
 struct MMWs {
@@ -121,56 +136,68 @@ MMWs mm_workspace(const moe_mm_shape* s, bool grouped) {
   return w;
 }
 
-// dx = dz W, dw = dz^T x on the given dz, and `sum` (may be empty)
-moe_status products_backward(const moe_mm_shape* s, const void* dz, const void* x, const void* w,
-                             const int32_t* offsets, const int32_t* slot, void* dx, int dx_dtype,
-                             void* dw, int dw_dtype, uint8_t* parts, const moe::PartSum& sum,
-                             hipStream_t st) {
-  const bool fp16 = s->dtype == MOE_FP16;
+// The launches of dx = dz W and dw = dz^T x on a given dz, and of `sum` (may be empty).
+struct Products {
+  moe::MMBackwardPlan plan;
+  bool fp16;
+  moe::MMArgs nn, tn;   // C NULL: not asked for
+  moe::SplitSum sum_dx, sum_dw;
+  moe::PartSum sum;
+};
+
+Products products_backward(const moe_mm_shape* s, const void* dz, const void* x, const void* w,
+                           const int32_t* offsets, const int32_t* slot, void* dx, int dx_dtype,
+                           void* dw, int dw_dtype, uint8_t* parts, const moe::PartSum& sum) {
+  Products p = {moe::mm_backward_plan(s->rows, offsets ? s->E : 0, s->N, s->K), s->dtype == MOE_FP16,
+                mm_args(s, offsets, nullptr), mm_args(s, offsets, slot), {}, {}, sum};
   if (s->rows == 0) dx = nullptr;
-  const moe::MMBackwardPlan plan = moe::mm_backward_plan(s->rows, offsets ? s->E : 0, s->N, s->K);
-  moe::MMArgs nn = mm_args(s, offsets, nullptr);
+  moe::MMArgs& nn = p.nn;
   nn.A = dz;
   nn.B = w;
   nn.C = dx;
   nn.ndim = s->K;
   nn.kdim = s->N;
   nn.c_f32 = dx_dtype == MOE_F32;
-  moe::MMArgs tn = mm_args(s, offsets, slot);
+  moe::MMArgs& tn = p.tn;
   tn.A = dz;
   tn.B = x;
   tn.C = dw;
   tn.mdim = s->N;
   tn.ndim = s->K;
   tn.c_f32 = dw_dtype == MOE_F32;
-  moe::SplitSum sum_dx = {}, sum_dw = {};
-  if (dw && plan.tn_splits > 1) {
-    tn.splits = plan.tn_splits;
+  if (dw && p.plan.tn_splits > 1) {
+    tn.splits = p.plan.tn_splits;
     tn.C = parts;
     tn.c_f32 = 1;
-    sum_dw = {reinterpret_cast<const float*>(parts), tn.splits, tn.E,
-              static_cast<long long>(s->N) * s->K, dw, dw_dtype};
+    p.sum_dw = {reinterpret_cast<const float*>(parts), tn.splits, tn.E,
+                static_cast<long long>(s->N) * s->K, dw, dw_dtype};
     parts += align256(static_cast<size_t>(tn.E) * tn.splits * s->N * s->K * 4);
   }
-  if (dx && plan.nn_splits > 1) {
-    nn.splits = plan.nn_splits;
+  if (dx && p.plan.nn_splits > 1) {
+    nn.splits = p.plan.nn_splits;
     nn.C = parts;
     nn.c_f32 = 1;
-    sum_dx = {reinterpret_cast<const float*>(parts), nn.splits, 1,
-              static_cast<long long>(s->rows) * s->K, dx, dx_dtype};
+    p.sum_dx = {reinterpret_cast<const float*>(parts), nn.splits, 1,
+                static_cast<long long>(s->rows) * s->K, dx, dx_dtype};
   }
-  const bool last = sum_dx.out || sum_dw.out;   // a launch of sums at the end
-  moe_status r;
-  if (dx && dw && plan.pair) {
-    r = launched(moe::launch_mm_pair(nn, tn, last ? moe::PartSum{} : sum, plan.pair, fp16, st),
-                 "gradient launch");
-    if (r || !last) return r;
+  return p;
+}
+
+// check: only whether every launch fits (see too_large).
+moe_status run_products(const Products& p, hipStream_t st, bool check) {
+  const bool last = p.sum_dx.out || p.sum_dw.out;   // a launch of sums at the end
+  hipError_t e = hipSuccess;
+  const bool pair = p.nn.C && p.tn.C && p.plan.pair;
+  if (pair) {
+    e = moe::launch_mm_pair(p.nn, p.tn, last ? moe::PartSum{} : p.sum, p.plan.pair, p.fp16, st, check);
   } else {
-    if (dx && (r = launched(moe::launch_mm_nn(nn, plan.nn, fp16, st), "row gradient launch"))) return r;
-    if (dw && (r = launched(moe::launch_mm_tn(tn, plan.tn, fp16, st), "weight gradient launch")))
-      return r;
+    if (p.nn.C) e = moe::launch_mm_nn(p.nn, p.plan.nn, p.fp16, st, check);
+    if (e == hipSuccess && p.tn.C) e = moe::launch_mm_tn(p.tn, p.plan.tn, p.fp16, st, check);
   }
-  return launched(moe::launch_sums(sum_dx, sum_dw, sum, st), "gradient sum launch");
+  if (check) return too_large(e);
+  if (e != hipSuccess) return launched(e, "gradient launch");
+  if (pair && !last) return MOE_OK;   // the sum went along
+  return launched(moe::launch_sums(p.sum_dx, p.sum_dw, p.sum, st), "gradient sum launch");
 }
 
 }  // namespace
@@ -198,7 +225,6 @@ moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* 
                            {"expert_offsets", expert_offsets, (shape->E + 1) * size_t{4}, false},
                            {"sorted_slot", sorted_slot, shape->rows * size_t{4}, false}})))
     return st;
-  if ((st = check_device()) != MOE_OK) return st;
   moe::MMArgs a = mm_args(shape, expert_offsets, sorted_slot);
   a.A = x;
   a.B = w;
@@ -208,8 +234,7 @@ moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, const void* 
   a.kdim = shape->K;
   a.act = shape->act;
   a.c_f32 = y_dtype == MOE_F32;
-  return launched(moe::launch_mm_nt(a, shape->dtype == MOE_FP16, static_cast<hipStream_t>(stream)),
-                  "moe_grouped_mm launch");
+  return run_forward(a, shape, stream, "moe_grouped_mm launch");
 }
 
 size_t moe_grouped_mm_backward_workspace(const moe_mm_shape* shape) {
@@ -258,20 +283,21 @@ moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy, co
                            {"expert_offsets", expert_offsets, (shape->E + 1) * size_t{4}, false},
                            {"sorted_slot", sorted_slot, rows * size_t{4}, false}})))
     return st;
-  if ((st = check_device()) != MOE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  const void* dz = dy;
-  if (shape->act != MOE_ACT_NONE) {
-    void* out = base + need.dz;
+  void* own = shape->act != MOE_ACT_NONE ? base + need.dz : nullptr;   // dz, where it is not dy
+  const Products p = products_backward(shape, own ? own : dy, x, w, expert_offsets,
+                                       shape->rows > 0 ? sorted_slot : nullptr, dx, dx_dtype, dw,
+                                       dw_dtype, base + need.parts, {});
+  if ((st = run_products(p, s, true))) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  if (own) {
     st = launched(moe::launch_dz(dy, false, z, expert_offsets, shape->E, shape->rows, shape->N,
-                                 shape->act, shape->dtype == MOE_FP16, out, nullptr, false, s),
+                                 shape->act, shape->dtype == MOE_FP16, own, nullptr, false, s),
                   "activation gradient launch");
     if (st) return st;
-    dz = out;
   }
-  return products_backward(shape, dz, x, w, expert_offsets, shape->rows > 0 ? sorted_slot : nullptr,
-                           dx, dx_dtype, dw, dw_dtype, base + need.parts, {}, s);
+  return run_products(p, s, false);
 }
 
 moe_status moe_linear(const moe_mm_shape* shape, const void* x, const void* w, const void* bias,
@@ -295,7 +321,6 @@ moe_status moe_linear(const moe_mm_shape* shape, const void* x, const void* w, c
                            {"bias", bias, values(1, shape->N, t), false},
                            {"residual", residual == y ? nullptr : residual, y_bytes, false}})))
     return st;
-  if ((st = check_device()) != MOE_OK) return st;
   moe::MMArgs a = mm_args(shape, nullptr, nullptr);
   a.A = x;
   a.B = w;
@@ -307,8 +332,7 @@ moe_status moe_linear(const moe_mm_shape* shape, const void* x, const void* w, c
   a.kdim = shape->K;
   a.act = shape->act;
   a.c_f32 = y_dtype == MOE_F32;
-  return launched(moe::launch_mm_nt(a, shape->dtype == MOE_FP16, static_cast<hipStream_t>(stream)),
-                  "moe_linear launch");
+  return run_forward(a, shape, stream, "moe_linear launch");
 }
 
 size_t moe_linear_backward_workspace(const moe_mm_shape* shape) {
@@ -353,25 +377,26 @@ moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_
                            {"w", w, values(shape->N, shape->K, t), false},
                            {"z", z, values(rows, shape->N, t), false}})))
     return st;
-  if ((st = check_device()) != MOE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   // dy itself is dz where no activation and no rounding stands between them
   const bool pass = shape->act != MOE_ACT_NONE || dy_dtype == MOE_F32;
-  const bool want_dz = pass && (dx || dw);
+  void* own = pass && (dx || dw) ? base + need.dz : nullptr;
   float* strips = dbias ? reinterpret_cast<float*>(base + need.strips) : nullptr;
-  const void* dz = want_dz ? base + need.dz : dy;
-  if (want_dz || dbias) {
+  const moe::PartSum sum = {strips, dbias ? moe::dz_strips(shape->rows, shape->N, shape->act) : 0,
+                            shape->N, dbias, dw_dtype};
+  const Products p = products_backward(shape, own ? own : dy, x, w, nullptr, nullptr, dx, dx_dtype,
+                                       dw, dw_dtype, base + need.parts, sum);
+  if ((st = run_products(p, s, true))) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  if (own || dbias) {
     st = launched(moe::launch_dz(dy, dy_dtype == MOE_F32, z, nullptr, 1, shape->rows, shape->N,
-                                 shape->act, shape->dtype == MOE_FP16,
-                                 want_dz ? base + need.dz : nullptr, strips, dw_dtype == MOE_F32, s),
+                                 shape->act, shape->dtype == MOE_FP16, own, strips,
+                                 dw_dtype == MOE_F32, s),
                   "activation gradient launch");
     if (st) return st;
   }
-  const moe::PartSum sum = {strips, dbias ? moe::dz_strips(shape->rows, shape->N, shape->act) : 0,
-                            shape->N, dbias, dw_dtype};
-  return products_backward(shape, dz, x, w, nullptr, nullptr, dx, dx_dtype, dw, dw_dtype,
-                           base + need.parts, sum, s);
+  return run_products(p, s, false);
 }
 
 static moe_status check_norm(const moe_norm_shape* s) {

@@ -7,10 +7,15 @@
 
 namespace moe {
 
+// Launches of products. check: nothing is launched and no device is asked; returns
+// hipErrorInvalidConfiguration where the launch would hold 2^32 threads or more.
 struct MMArgs;
-hipError_t launch_mm_nt(const MMArgs& a, bool fp16, hipStream_t s);
-hipError_t launch_mm_nn(const MMArgs& a, int geom, bool fp16, hipStream_t s);
-hipError_t launch_mm_tn(const MMArgs& a, int geom, bool fp16, hipStream_t s);
+hipError_t launch_mm_nt(const MMArgs& a, int plan, bool fp16, hipStream_t s, bool check);
+hipError_t launch_mm_nn(const MMArgs& a, int geom, bool fp16, hipStream_t s, bool check);
+hipError_t launch_mm_tn(const MMArgs& a, int geom, bool fp16, hipStream_t s, bool check);
+// The kernel of a forward product (launch_mm_nt's `plan`): 0 to 5 mm_pick_rows's
+// geometries, 6 and 7 the few-row kernel with 16 and 32 rows a block. E 0: no experts.
+int mm_forward_plan(int rows, int E, int N, int K, int act);
 // out[n] = sum of part[parts][n] in order; out_type 0 bf16, 1 fp16, 2 float32.
 // out NULL: none.
 struct PartSum {
@@ -31,7 +36,7 @@ MMBackwardPlan mm_backward_plan(int rows, int E, int N, int K);   // E 0: no exp
 size_t mm_backward_parts(int rows, int E, int N, int K);
 // Both gradients, and a sum, in one launch.
 hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
-                          bool fp16, hipStream_t s);
+                          bool fp16, hipStream_t s, bool check);
 
 // dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
 // (part [dz_strips(rows, N, act)][N], may be NULL). offsets NULL: all rows; otherwise

@@ -178,7 +178,7 @@ inline double mm_few_cost(int mt, int rows, int E, int ndim, int kdim) {
 }
 
 template <class T, int MT, int WAVES, int U>
-hipError_t mm_few_launch(MMArgs a, hipStream_t s) {
+hipError_t mm_few_launch(MMArgs a, hipStream_t s, bool check) {
   const bool swiglu = a.act == kActSwiglu;
   a.nt = swiglu ? (a.ndim / 2 + 7) / 8 : (a.ndim + 15) / 16;
   const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
@@ -186,6 +186,7 @@ hipError_t mm_few_launch(MMArgs a, hipStream_t s) {
   if (grid == 0) return hipSuccess;
   if (!mm_fits(grid, WAVES * 64, (a.rows / (16 * MT) + 1LL) * a.nt, a.E))
     return hipErrorInvalidConfiguration;
+  if (check) return hipSuccess;
   hipLaunchKernelGGL((mm_few_kernel<T, MT, WAVES, U>), dim3(static_cast<unsigned>(grid)),
                      dim3(WAVES * 64), 0, s, static_cast<const uint8_t*>(a.A),
                      static_cast<const uint8_t*>(a.B), a);

@@ -23,11 +23,12 @@ __global__ __launch_bounds__(G::kThreads, G::WPE) void mm_pair_kernel(
 }
 
 template <class T, class G>
-hipError_t launch(MMArgs nn, MMArgs tn, const PartSum& sum, hipStream_t s) {
+hipError_t launch(MMArgs nn, MMArgs tn, const PartSum& sum, hipStream_t s, bool check) {
   const long long tb = mm_prepare<kModeTN, G>(tn), nb = mm_prepare<kModeNN, G>(nn),
                   grid = tb + nb + sum_parts_blocks(sum);
   if (!mm_fits(grid, G::kThreads, (nn.rows / G::BM + 1LL) * nn.nt * nn.splits, nn.E))
     return hipErrorInvalidConfiguration;
+  if (check) return hipSuccess;
   static MMReady ready;
   const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_pair_kernel<T, G>), G::kLds);
   if (e != hipSuccess) return e;
@@ -125,10 +126,12 @@ size_t mm_backward_parts(int rows, int E, int N, int K) {
 }
 
 hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
-                          bool fp16, hipStream_t s) {
+                          bool fp16, hipStream_t s, bool check) {
   if (pair == 1)
-    return fp16 ? launch<fp16_tag, MMMid>(nn, tn, sum, s) : launch<bf16_tag, MMMid>(nn, tn, sum, s);
-  return fp16 ? launch<fp16_tag, MMSmall>(nn, tn, sum, s) : launch<bf16_tag, MMSmall>(nn, tn, sum, s);
+    return fp16 ? launch<fp16_tag, MMMid>(nn, tn, sum, s, check)
+                : launch<bf16_tag, MMMid>(nn, tn, sum, s, check);
+  return fp16 ? launch<fp16_tag, MMSmall>(nn, tn, sum, s, check)
+              : launch<bf16_tag, MMSmall>(nn, tn, sum, s, check);
 }
 
 }  // namespace moe
