@@ -307,11 +307,8 @@ __device__ __forceinline__ void mm_interleave() {
 
 constexpr uint32_t kMMPastEnd = 0x80000000u;   // at or past the end of every resource here
 
-// Whether a launch fits: under 2^32 threads, and under 2^31 tiles whatever the
-// offsets hold (each of E experts all the rows).
-inline bool mm_fits(long long grid, int threads, long long expert_tiles, int E) {
-  return grid * threads < (1LL << 32) && expert_tiles * E < (1LL << 31);
-}
+// Whether a launch fits: under 2^32 threads, so under 2^26 tiles.
+inline bool mm_fits(long long grid, int threads) { return grid * threads < (1LL << 32); }
 constexpr int kMMSegRows = 1024;               // TN gather: source rows held in LDS at a time
 constexpr int kMMGroupM = 8;                   // m tiles walked together over all n tiles
 
@@ -321,6 +318,10 @@ constexpr int kMMGroupM = 8;                   // m tiles walked together over a
 // it holds at one time share W strips and x rows in its L2. Offsets are clamped
 // to [0, rows] and a block's end to its start, so that values outside the
 // contract cannot lead out of the buffers. Returns false for a block without a tile.
+// Counts are unsigned: an expert's tiles stay under 2^31 for any offsets, but where
+// blocks overlap (outside the contract) their sum may wrap, so that a block finds
+// several experts, or none. Each of the four values it reads is one that some expert
+// wrote, and the tile is checked against them.
 struct MMTile {
   int e, nt, p0, p1;   // rows [p0, p1), at most BM of them
 };
@@ -332,56 +333,60 @@ template <int BM, int NTHR>
 __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, int rows, int E,
                                              int NT, int* sm, uint32_t bid, MMTile& t) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid >> 6;
-  int e = 0, local = 0, mtiles = 0, beg = 0, end = 0;
+  int e = 0, mtiles = 0, beg = 0, end = 0;
+  uint32_t local = 0;
   if (offsets == nullptr) {
     mtiles = (rows + BM - 1) / BM;
-    const int total = mtiles * NT, chunk = (total + 7) / 8;
+    const uint32_t total = static_cast<uint32_t>(mtiles) * NT, chunk = (total + 7) / 8;
     local = (bid & 7) * chunk + (bid >> 3);
-    if (static_cast<int>(bid >> 3) >= chunk || local >= total) return false;
+    if ((bid >> 3) >= chunk || local >= total) return false;
     end = rows;
   } else {
     constexpr int kPer = 1024 / NTHR > 0 ? 1024 / NTHR : 1;   // E <= 1024
     const int ept = (E + NTHR - 1) / NTHR;
-    int cnt[kPer], b[kPer], n[kPer], sum = 0;
+    int* out = sm + NTHR / kWave;
+    int b[kPer], n[kPer];
+    uint32_t cnt[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int ei = tid * ept + i;
-      int c = 0, lo = 0, hi = 0;
+      int lo = 0, hi = 0;
+      uint32_t c = 0;
       if (i < ept && ei < E) {
         lo = min(max(offsets[ei], 0), rows);
         hi = min(max(offsets[ei + 1], lo), rows);
-        c = (hi - lo + BM - 1) / BM * NT;
+        c = static_cast<uint32_t>((hi - lo + BM - 1) / BM) * NT;
       }
       cnt[i] = c;
       b[i] = lo;
       n[i] = hi;
       sum += c;
     }
-    int incl = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
-      const int o = __shfl_up(incl, d, kWave);
+      const uint32_t o = __shfl_up(incl, d, kWave);
       if (lane >= d) incl += o;
     }
-    if (lane == kWave - 1) sm[wv] = incl;
+    if (lane == kWave - 1) sm[wv] = static_cast<int>(incl);
+    if (tid == 0) out[0] = -1;
     __syncthreads();
-    int before = 0, total = 0;
+    uint32_t before = 0, total = 0;
 #pragma unroll
     for (int i = 0; i < NTHR / kWave; ++i) {
-      const int s = sm[i];
+      const uint32_t s = sm[i];
       if (i < wv) before += s;
       total += s;
     }
-    const int chunk = (total + 7) / 8;
-    const int tau = (bid & 7) * chunk + (bid >> 3);
-    if (static_cast<int>(bid >> 3) >= chunk || tau >= total) return false;   // uniform
-    int start = before + incl - sum;
-    int* out = sm + NTHR / kWave;
+    const uint32_t chunk = total / 8 + (total % 8 != 0);
+    const uint32_t tau = (bid & 7) * chunk + (bid >> 3);
+    if ((bid >> 3) >= chunk || tau >= total) return false;   // uniform
+    uint32_t start = before + incl - sum;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if (tau >= start && tau < start + cnt[i]) {
+      if (tau - start < cnt[i]) {
         out[0] = tid * ept + i;
-        out[1] = tau - start;
+        out[1] = static_cast<int>(tau - start);
         out[2] = b[i];
         out[3] = n[i];
       }
@@ -392,9 +397,12 @@ __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, in
     local = __builtin_amdgcn_readfirstlane(out[1]);
     beg = __builtin_amdgcn_readfirstlane(out[2]);
     end = __builtin_amdgcn_readfirstlane(out[3]);
+    if (e < 0 || beg >= end) return false;
     mtiles = (end - beg + BM - 1) / BM;
+    if (local >= static_cast<uint32_t>(mtiles) * NT) return false;
   }
-  const int per = kMMGroupM * NT, g = local / per, r = local - g * per;
+  const int per = kMMGroupM * NT, g = static_cast<int>(local) / per,
+            r = static_cast<int>(local) - g * per;
   const int gm = min(kMMGroupM, mtiles - g * kMMGroupM);
   t.e = e;
   t.nt = r / gm;

@@ -184,8 +184,7 @@ hipError_t mm_few_launch(MMArgs a, hipStream_t s, bool check) {
   const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
   const long long grid = ((a.rows / (16 * MT) + partial) * a.nt + 7) / 8 * 8;
   if (grid == 0) return hipSuccess;
-  if (!mm_fits(grid, WAVES * 64, (a.rows / (16 * MT) + 1LL) * a.nt, a.E))
-    return hipErrorInvalidConfiguration;
+  if (!mm_fits(grid, WAVES * 64)) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;
   hipLaunchKernelGGL((mm_few_kernel<T, MT, WAVES, U>), dim3(static_cast<unsigned>(grid)),
                      dim3(WAVES * 64), 0, s, static_cast<const uint8_t*>(a.A),

@@ -160,8 +160,7 @@ template <class T, int MODE, class G>
 hipError_t mm_launch(MMArgs a, hipStream_t s, bool check) {
   const long long grid = mm_prepare<MODE, G>(a);
   if (grid == 0) return hipSuccess;
-  const long long each = MODE == kModeTN ? 0 : (a.rows / G::BM + 1LL) * a.nt * a.splits;
-  if (!mm_fits(grid, G::kThreads, each, a.E)) return hipErrorInvalidConfiguration;
+  if (!mm_fits(grid, G::kThreads)) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;
   static MMReady ready;
   const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_kernel<T, MODE, G>), G::kLds);

@@ -26,8 +26,7 @@ template <class T, class G>
 hipError_t launch(MMArgs nn, MMArgs tn, const PartSum& sum, hipStream_t s, bool check) {
   const long long tb = mm_prepare<kModeTN, G>(tn), nb = mm_prepare<kModeNN, G>(nn),
                   grid = tb + nb + sum_parts_blocks(sum);
-  if (!mm_fits(grid, G::kThreads, (nn.rows / G::BM + 1LL) * nn.nt * nn.splits, nn.E))
-    return hipErrorInvalidConfiguration;
+  if (!mm_fits(grid, G::kThreads)) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;
   static MMReady ready;
   const hipError_t e = ready.set(reinterpret_cast<const void*>(&mm_pair_kernel<T, G>), G::kLds);

@@ -50,3 +50,45 @@ def test_a_gradient_whose_launch_is_too_large_is_refused_first(act):
         assert b"2^32 threads" in LIB.moe_last_error()
     if NO_GPU:
         assert backward(s, True, dw=False) == EDEV and forward(s, True) == EDEV
+
+
+@pytest.mark.skipif(not NO_GPU, reason="would run")
+@pytest.mark.parametrize("rows,K,N", [(65536, 64, 262144), (65536, 8, 262144)])
+def test_tiles_are_counted_as_the_offsets_cut_them(rows, K, N):
+    """1024 experts share the rows: 2^20 tiles of 64x128 or less. That every expert held
+    all rows would be 2^31 of them."""
+    s = shape(rows, K, N, E=1024)
+    assert forward(s, True) == EDEV and backward(s, True, dw=False) == EDEV
+
+
+@pytest.mark.gpu
+def test_many_experts_and_many_columns():
+    """The same on the GPU: 65536 rows of 1024 uneven experts x 262144 columns."""
+    if NO_GPU:
+        pytest.skip("no GPU")
+    import quantized_moe_expert_top_amd as moe
+    E, rows, K, N, t = 1024, 65536, 8, 262144, torch.bfloat16
+    print("[case] many experts and columns", flush=True)
+    g = torch.Generator().manual_seed(2)
+    n = torch.rand(E, generator=g) ** 2
+    n[::7] = 0
+    n = (n / n.sum() * (rows - 5)).long()              # the last rows belong to no expert
+    off = [0] + torch.cumsum(n, 0).tolist()
+    gd = torch.Generator(device="cuda")
+    gd.manual_seed(3)
+    x = torch.randn((rows, K), generator=gd, device="cuda").to(t)
+    w = torch.randn((E, N, K), generator=gd, device="cuda").to(t)
+    y = torch.full((rows, N), float("nan"), dtype=t, device="cuda")
+    moe.grouped_mm(x, w, torch.tensor(off, dtype=torch.int32, device="cuda"), y)
+    torch.cuda.synchronize()
+    for a in range(0, off[-1], 4096):
+        assert not torch.isnan(y[a:min(a + 4096, off[-1])]).any(), a
+    assert torch.isnan(y[off[-1]:]).all()
+    for e in [i for i in range(E) if n[i]][::40] + [max(i for i in range(E) if n[i])]:
+        we = w[e].double()
+        for p in {off[e], off[e + 1] - 1}:
+            ref = we @ x[p].double()
+            mag = we.abs() @ x[p].double().abs()
+            # float32 sums of K products, one rounding to bf16
+            tol = (K + 2) * 2.0 ** -24 * mag + 2.0 ** -8 * ref.abs() + 2.0 ** -133
+            assert ((y[p].double() - ref).abs() <= tol).all(), (e, p)
