@@ -52,11 +52,12 @@ extern "C" {
 /*
  * Shape of a product. Let No = N/2 for MOE_ACT_SWIGLU and N otherwise.
  *   rows    rows of y (grouped: the capacity R of the grouped arrays), at most
- *           2^31 - 2^16; rows*max(N, K) <= 2^38, and a launch holds fewer than
- *           2^32 threads (64 rows x 64 columns take 256; MOE_ESHAPE otherwise,
- *           before any launch of the call)
+ *           2^31 - 2^16; rows*max(N, K) <= 2^38
  *   K, N    multiples of 8 (N of 16 for SWIGLU), N*K <= 2^30
- *   E       experts (1 .. MOE_MAX_EXPERTS); moe_linear* ignore it
+ *   E       experts (1 .. MOE_MAX_EXPERTS); moe_linear* ignore it. Weight
+ *           gradients: 256 rows x 256 columns of an expert's take 512 threads of
+ *           a launch that holds fewer than 2^32 (E*N*K below 2^39 where N and K
+ *           are multiples of 256); MOE_ESHAPE otherwise, before any launch
  *   x_rows  rows of x when sorted_slot is given (x_rows*K <= 2^30); otherwise
  *           x has `rows` rows and this is ignored
  *   topk    with sorted_slot: x's row for grouped row p is sorted_slot[p] / topk

@@ -307,8 +307,11 @@ __device__ __forceinline__ void mm_interleave() {
 
 constexpr uint32_t kMMPastEnd = 0x80000000u;   // at or past the end of every resource here
 
-// Whether a launch fits: under 2^32 threads, so under 2^26 tiles.
-inline bool mm_fits(long long grid, int threads) { return grid * threads < (1LL << 32); }
+// Whether a launch of `tiles` blocks (rounded up to eight, see mm_find_tile) fits:
+// under 2^32 threads, so under 2^26 tiles.
+inline bool mm_fits(long long tiles, int threads) {
+  return (tiles + 7) / 8 * 8 * threads < (1LL << 32);
+}
 constexpr int kMMSegRows = 1024;               // TN gather: source rows held in LDS at a time
 constexpr int kMMGroupM = 8;                   // m tiles walked together over all n tiles
 

@@ -171,6 +171,7 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
 inline double mm_few_cost(int mt, int rows, int E, int ndim, int kdim) {
   const double tiles = mm_row_tiles(16 * mt, rows, E), blocks = tiles * ((ndim + 15) / 16);
   if (E != 0 && blocks > 1024) return 1e300;
+  if (!mm_fits(mm_most_row_tiles(16 * mt, rows, E) * ((ndim + 15) / 16), 512)) return 1e300;
   const double fill = rows / (tiles * 16 * mt);
   const double step = (mt == 1 ? 0.072 : 0.104) * (0.5 + 0.5 * fill), start = mt == 1 ? 3.4 : 4.2;
   const double rounds = __builtin_ceil(blocks / 256);
@@ -181,8 +182,8 @@ template <class T, int MT, int WAVES, int U>
 hipError_t mm_few_launch(MMArgs a, hipStream_t s, bool check) {
   const bool swiglu = a.act == kActSwiglu;
   a.nt = swiglu ? (a.ndim / 2 + 7) / 8 : (a.ndim + 15) / 16;
-  const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
-  const long long grid = ((a.rows / (16 * MT) + partial) * a.nt + 7) / 8 * 8;
+  const long long tiles = mm_most_row_tiles(16 * MT, a.rows, a.offsets ? a.E : 0) * a.nt;
+  const long long grid = (tiles + 7) / 8 * 8;
   if (grid == 0) return hipSuccess;
   if (!mm_fits(grid, WAVES * 64)) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;

@@ -11,7 +11,7 @@ namespace moe {
 // 387 us), faster where a tile has few stages (128 experts x 1536 x 2048 from
 // 32768 rows: 311 against 343 us; from 4096 rows: 159 against 207).
 using MMTall = MMGeom<256, 128, 2, 2, 32, 2, 2>;
-constexpr MMCost kMMTallCost = {256, 128, 512, 1.00, 1.20, 1.89, 5.4, 5.4, 5.4};
+constexpr MMCost kMMTallCost = {256, 128, 256, 512, 1.00, 1.20, 1.89, 5.4, 5.4, 5.4};
 
 // A product's geometry and the number of parts that its contraction is cut into:
 // where the output tiles alone leave CUs idle each part is a float32 product in the
@@ -60,6 +60,7 @@ inline MMPlan mm_plan_tn(int rows, int E, int mdim, int ndim, bool split) {
     const MMCost& c = *table[i];
     const double tiles = static_cast<double>(E) * ((mdim + c.bm - 1) / c.bm) *
                          ((ndim + c.bn - 1) / c.bn);
+    if (!mm_fits(static_cast<long long>(tiles) * most, c.threads)) continue;
     for (int s = split ? 2 : 1; s <= most; s *= 2) {
       const double cost = mm_cost(c, tiles * s, stages / s) +
                           mm_split_cost(static_cast<double>(E) * mdim * ndim, s);

@@ -37,15 +37,15 @@ using MMDeep = MMGeom<128, 128, 2, 4, 64, 4, 2>;
 //       grouped, 128 experts, 32768 x 2048 x 768    Big 172 (205)   Mid 205 (214)
 //   TN  1536 x 2048 x 4096   Big 83 (85)     Mid 45 (41)    Small 52 (50)
 struct MMCost {
-  int bm, bn, slots;
+  int bm, bn, threads, slots;
   double s1, s2, s3, full, part, dense;
 };
-constexpr MMCost kMMBigCost = {256, 256, 256, 1.12, 1.64, 1.64, 9.0, 9.0, 14.0};
-constexpr MMCost kMMMidCost = {128, 128, 512, 0.62, 0.66, 0.96, 9.0, 4.0, 7.5};
-constexpr MMCost kMMWideCost = {64, 128, 512, 0.30, 0.36, 0.65, 6.5, 3.8, 2.3};
-constexpr MMCost kMMSmallCost = {64, 64, 512, 0.20, 0.23, 0.40, 5.0, 3.5, 1.7};
-constexpr MMCost kMMLongCost = {128, 256, 512, 1.00, 1.20, 1.90, 11.0, 5.0, 12.0};
-constexpr MMCost kMMDeepCost = {128, 128, 256, 0.41, 0.61, 0.61, 6.0, 4.0, 4.5};
+constexpr MMCost kMMBigCost = {256, 256, 512, 256, 1.12, 1.64, 1.64, 9.0, 9.0, 14.0};
+constexpr MMCost kMMMidCost = {128, 128, 256, 512, 0.62, 0.66, 0.96, 9.0, 4.0, 7.5};
+constexpr MMCost kMMWideCost = {64, 128, 512, 512, 0.30, 0.36, 0.65, 6.5, 3.8, 2.3};
+constexpr MMCost kMMSmallCost = {64, 64, 256, 512, 0.20, 0.23, 0.40, 5.0, 3.5, 1.7};
+constexpr MMCost kMMLongCost = {128, 256, 256, 512, 1.00, 1.20, 1.90, 11.0, 5.0, 12.0};
+constexpr MMCost kMMDeepCost = {128, 128, 512, 256, 0.41, 0.61, 0.61, 6.0, 4.0, 4.5};
 
 // m tiles of row blocks: of `rows` rows in one block (E = 0), or spread over E
 // experts, where about half a tile per expert in use is left over and none has
@@ -54,6 +54,11 @@ inline double mm_row_tiles(int bm, int rows, int E) {
   if (E == 0) return (rows + bm - 1) / bm;
   const double act = rows < E ? rows : E, n = static_cast<double>(rows) / bm + 0.5 * act;
   return n > act ? n : act;
+}
+// Most blocks of row-grouped tiles over all ways to cut the rows: a partial tile per
+// expert (E 0: no experts).
+inline long long mm_most_row_tiles(int bm, int rows, int E) {
+  return rows / bm + (E == 0 ? 1LL : rows < E ? rows : E);
 }
 // Dense: `epi` us per 65536 results of a CU for activations.
 inline double mm_cost(const MMCost& c, double tiles, double stages, bool dense = false,
@@ -89,7 +94,9 @@ inline MMPick mm_pick_rows(int rows, int E, int ndim, int kdim, int act = 0) {
   for (int i = 0; i < (E == 0 ? 6 : 5); ++i) {
     const MMCost& c = *table[i];
     if (low && c.bm > 64) continue;
-    const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * ((ndim + c.bn - 1) / c.bn),
+    const int nt = (ndim + c.bn - 1) / c.bn;
+    if (!mm_fits(mm_most_row_tiles(c.bm, rows, E) * nt, c.threads)) continue;
+    const double cost = mm_cost(c, mm_row_tiles(c.bm, rows, E) * nt,
                                 (kdim + 63) / 64, E == 0, epi);
     if (cost < best.cost) best = {i, cost};
   }
@@ -131,9 +138,7 @@ long long mm_prepare(MMArgs& a) {
     mm_set_stream(a, static_cast<long long>(a.E) * a.splits * a.mdim, a.ndim);
   } else {
     mm_set_stream(a, static_cast<long long>(a.rows) * a.splits, swiglu ? a.ndim / 2 : a.ndim);
-    // an upper bound over all ways to cut the rows: a partial tile per expert
-    const long long partial = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;
-    tiles = (a.rows / G::BM + partial) * a.nt * a.splits;
+    tiles = mm_most_row_tiles(G::BM, a.rows, a.offsets ? a.E : 0) * a.nt * a.splits;
   }
   return (tiles + 7) / 8 * 8;
 }

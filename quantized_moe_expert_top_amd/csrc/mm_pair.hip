@@ -80,6 +80,10 @@ static MMBackwardPlan plan_of(int rows, int E, int N, int K) {
     const double kt = (K + c.bn - 1) / c.bn;
     const double tn_tiles = groups * static_cast<double>((N + c.bm - 1) / c.bm) * kt,
                  nn_tiles = mm_row_tiles(c.bm, rows, E) * kt;
+    if (!mm_fits(static_cast<long long>(tn_tiles) * most_dw +
+                     mm_most_row_tiles(c.bm, rows, E) * static_cast<long long>(kt) * most_dx +
+                     (N + 31) / 32 + 16, c.threads))
+      continue;
     for (int a = 1; a <= most_dx; a *= 2)
       for (int b = 1; b <= most_dw; b *= 2) {
         const double cost = pair_cost(c, tn_tiles * b, tn_stages / b, nn_tiles * a, nn_stages / a) +

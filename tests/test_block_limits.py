@@ -92,3 +92,49 @@ def test_many_experts_and_many_columns():
             # float32 sums of K products, one rounding to bf16
             tol = (K + 2) * 2.0 ** -24 * mag + 2.0 ** -8 * ref.abs() + 2.0 ** -133
             assert ((y[p].double() - ref).abs() <= tol).all(), (e, p)
+
+
+@pytest.mark.skipif(not NO_GPU, reason="would run")
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("act", [0, 2, 3, 4])
+@pytest.mark.parametrize("K,N", [(8, 16), (16, 16), (128, 128), (8, 128), (128, 16)])
+def test_rows_up_to_the_limit_find_a_kernel_that_fits(K, N, act, grouped):
+    """A row takes at least two threads (256 x 256 columns in 512), so every count of rows
+    that the shape allows has a launch, whichever kernel would be fastest."""
+    for rows in ((1 << 31) - (1 << 16), (1 << 30) + 77, (1 << 29) + 1, (1 << 28) + 1, 1 << 27):
+        s = shape(rows, K, N, E=3, act=act)
+        assert forward(s, grouped) == EDEV, (rows, LIB.moe_last_error())
+        assert backward(s, grouped) == EDEV, (rows, LIB.moe_last_error())
+        assert backward(s, grouped, dw=False) == EDEV, (rows, LIB.moe_last_error())
+
+
+@pytest.mark.gpu
+def test_more_than_a_billion_rows():
+    """2^30 rows and more of 8 columns to 16: equal rows give equal results wherever they
+    stand, and those of the first period are checked."""
+    if NO_GPU:
+        pytest.skip("no GPU")
+    import quantized_moe_expert_top_amd as moe
+    period, rep, K, N, t = 65537, 16384, 8, 16, torch.bfloat16
+    print("[case] a billion rows", flush=True)
+    gd = torch.Generator(device="cuda")
+    gd.manual_seed(5)
+    xp = torch.randn((period, K), generator=gd, device="cuda").to(t)
+    w = torch.randn((N, K), generator=gd, device="cuda").to(t)
+    x = xp.repeat(rep, 1)
+    y = torch.full((period * rep, N // 2), float("nan"), dtype=t, device="cuda")
+    moe.linear(x, w, y, act="swiglu")
+    torch.cuda.synchronize()
+    z = xp.double() @ w.double().t()
+    ez = (K + 2) * 2.0 ** -24 * (xp.double().abs() @ w.double().abs().t())
+    g, u = z.chunk(2, -1)
+    eg, eu = ez.chunk(2, -1)
+    s = g / (1 + torch.exp(-g))
+    # |silu'| <= 1.1; silu with one exp2 off by |g| 2^-24 more than 10 float32 roundings
+    es = 1.1 * eg + (10 + g.abs()) * 2.0 ** -24 * s.abs()
+    tol = (es * (u.abs() + eu) + s.abs() * eu) * (1 + 2.0 ** -8) + 2.0 ** -8 * (s * u).abs() + 2.0 ** -133
+    first = y[:period]
+    assert ((first.double() - s * u).abs() <= tol).all()
+    v = y.view(rep, period, N // 2)
+    for a in range(0, rep, 512):
+        assert (v[a:a + 512] == first).all(), a
