@@ -153,6 +153,21 @@ MOE_API moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy
                                        void* dbias, int32_t dw_dtype, void* ws, size_t ws_bytes,
                                        void* stream);
 
+/*
+ * moe_product_plan — the kernels that a product of this shape and its gradients run
+ * on, chosen by estimated time from the shape alone. Host only; for tests and tuning:
+ * the numbers may change between versions.
+ *   grouped   nonzero: moe_grouped_mm's, else moe_linear's
+ *   plan      int32 [6], written:
+ *     [0]  forward: 0 tiles of 256x256, 1 128x128, 2 64x128, 3 64x64, 4 128x256,
+ *          5 128x128 of four stages, 6 and 7 rows by 16 and by 32
+ *     [1]  gradients: 0 each in a launch of its own; both in one launch (where both
+ *          are asked for) of 1 128x128 or 2 64x64 tiles
+ *     [2]  dx's tiles in a launch of its own (numbers as in [0]);  [3] its parts
+ *     [4]  dw's: 0 256x256, 1 256x128, 2 128x128, 3 64x64;  [5] its parts
+ */
+MOE_API moe_status moe_product_plan(const moe_mm_shape* shape, int32_t grouped, int32_t* plan);
+
 /* How block_norm's gate broadcasts over y [T, H]. */
 #define MOE_GATE_NONE 0
 #define MOE_GATE_CHANNEL 1 /* gate [H]    */

@@ -19,7 +19,7 @@ from ._lib import (  # noqa: F401
 from ._block import (  # noqa: F401
     block_norm, block_norm_backward, block_norm_backward_workspace, combine_backward, grouped_mm,
     grouped_mm_backward, grouped_mm_backward_workspace, linear, linear_backward,
-    linear_backward_workspace,
+    linear_backward_workspace, product_plan,
 )
 
 __all__ = ["MoeError", "LayerBuffers", "moe_forward", "moe_layer", "load", "router_logits",
@@ -27,7 +27,7 @@ __all__ = ["MoeError", "LayerBuffers", "moe_forward", "moe_layer", "load", "rout
            "permute", "grouped_w4a16_ffn", "grouped_w4a8_ffn", "grouped_w8a8_ffn", "combine",
            "layer_w4a16", "layer_w4a16_noalloc", "expert_counts_accumulate", "expert_hot_rank",
            "grouped_mm", "grouped_mm_backward", "linear", "linear_backward", "block_norm",
-           "block_norm_backward", "combine_backward"]
+           "block_norm_backward", "combine_backward", "product_plan"]
 
 
 @dataclass

@@ -19,7 +19,7 @@ from ._lib import _check
 EXPORTS = ("moe_grouped_mm", "moe_grouped_mm_backward_workspace", "moe_grouped_mm_backward",
            "moe_linear", "moe_linear_backward_workspace", "moe_linear_backward",
            "moe_block_norm", "moe_block_norm_backward_workspace", "moe_block_norm_backward",
-           "moe_combine_backward")
+           "moe_combine_backward", "moe_product_plan")
 
 BF16, FP16, F32 = 0, 1, 2
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
@@ -59,6 +59,7 @@ def _load() -> ctypes.CDLL:
             "moe_block_norm": (INT, [norm] + [P] * 8),
             "moe_block_norm_backward_workspace": (SZ, [I32, I32]),
             "moe_block_norm_backward": (INT, [norm] + [P] * 13 + [SZ, P]),
+            "moe_product_plan": (INT, [mm, I32, P]),
             "moe_combine_backward": (INT, [P] * 5 + [I32] * 4 + [P, I32, P, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -172,6 +173,24 @@ def linear_backward(dy, x, w, dx=None, dw=None, dbias=None, act: str = "none", z
     st = (_binding or _ext()).linear_backward(*args)
     if st:
         _done("moe_linear_backward", st, lambda: _binding.linear_backward(*args))
+
+
+_TILES = ("256x256", "128x128", "64x128", "64x64", "128x256", "128x128 deep", "rows by 16",
+          "rows by 32")
+_DW_TILES = ("256x256", "256x128", "128x128", "64x64")
+
+
+def product_plan(rows: int, K: int, N: int, E: int = 0, act: str = "none") -> dict:
+    """The kernels that linear (E = 0) or grouped_mm and their gradients run on for
+    this shape, for tests and tuning: forward, dx and dw name tiles, dx_parts and
+    dw_parts count the parts of their contractions, together names the tiles of the
+    one launch for both gradients (None: each in its own)."""
+    s = MoeMMShape(rows, K, N, E or 1, 0, 1, BF16, _act(act))
+    plan = (ctypes.c_int32 * 6)()
+    _check("moe_product_plan", _load().moe_product_plan(ctypes.byref(s), E > 0, plan))
+    f, pair, dx, dx_parts, dw, dw_parts = plan
+    return dict(forward=_TILES[f], together=(None, "128x128", "64x64")[pair], dx=_TILES[dx],
+                dx_parts=dx_parts, dw=_DW_TILES[dw], dw_parts=dw_parts)
 
 
 def block_norm(r, y=None, r_out=None, h=None, w_post=None, w_pre=None, gate=None,

@@ -399,6 +399,18 @@ moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy, int32_
   return run_products(p, s, false);
 }
 
+moe_status moe_product_plan(const moe_mm_shape* shape, int32_t grouped, int32_t* plan) {
+  const moe_status st = check_mm(shape, grouped != 0);
+  if (st) return st;
+  if (!plan) return fail(MOE_EINVAL, "plan is NULL");
+  const int E = grouped ? shape->E : 0;
+  const moe::MMBackwardPlan b = moe::mm_backward_plan(shape->rows, E, shape->N, shape->K);
+  const int32_t v[6] = {moe::mm_forward_plan(shape->rows, E, shape->N, shape->K, shape->act),
+                        b.pair, b.nn, b.nn_splits, b.tn, b.tn_splits};
+  for (int i = 0; i < 6; ++i) plan[i] = v[i];
+  return MOE_OK;
+}
+
 static moe_status check_norm(const moe_norm_shape* s) {
   if (!s) return fail(MOE_EINVAL, "shape is NULL");
   if (s->T < 0) return fail(MOE_EINVAL, "T = %d < 0", s->T);
