@@ -38,23 +38,18 @@ constexpr int kDzCols = 512;
 template <class T, bool SWIGLU, bool EXACT>
 __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, int dy_f32,
                                                  const void* __restrict__ z,
-                                                 const int* __restrict__ offsets, int E, int rows,
-                                                 int N, int act, int strip_rows, int col_blocks,
-                                                 void* __restrict__ dz, float* __restrict__ part) {
+                                                 int rows, int N, int act, int strip_rows,
+                                                 int col_blocks, void* __restrict__ dz,
+                                                 float* __restrict__ part) {
   constexpr int S = SWIGLU ? 2 : 1;
   __shared__ float red[3][S][kDzCols];
   const int No = SWIGLU ? N / 2 : N;
   const int cb = blockIdx.x % col_blocks, strip = blockIdx.x / col_blocks;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   const int col = cb * kDzCols + tx * 8;
-  int lo = 0, hi = rows;
-  if (offsets) {
-    lo = min(max(offsets[0], 0), rows);
-    hi = min(max(offsets[E], lo), rows);
-  }
   // 64-bit: the last strip's end may pass 2^31
   const long long r0 = static_cast<long long>(strip) * strip_rows;
-  const long long r1 = min(r0 + strip_rows, static_cast<long long>(hi));
+  const long long r1 = min(r0 + strip_rows, static_cast<long long>(rows));
   float sum[S][8];
 #pragma unroll
   for (int s = 0; s < S; ++s)
@@ -62,7 +57,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, in
     for (int i = 0; i < 8; ++i) sum[s][i] = 0.0f;
   if (col < No) {
 #pragma unroll 2
-    for (long long r = max(r0, static_cast<long long>(lo)) + ty; r < r1; r += 4) {
+    for (long long r = r0 + ty; r < r1; r += 4) {
       float d[8], g[8];
       load8<T>(dy, r * No + col, dy_f32, d);
       if (SWIGLU) {
@@ -89,7 +84,6 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, in
       for (int i = 0; i < 8; ++i) sum[0][i] += d[i];
     }
   }
-  if (part == nullptr) return;
   if (ty > 0)
 #pragma unroll
     for (int s = 0; s < S; ++s)
@@ -238,7 +232,7 @@ hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offs
   }
   auto run = [&](auto tag, auto swiglu, auto exact) {
     dz_kernel<decltype(tag), decltype(swiglu)::value, decltype(exact)::value>
-        <<<grid, block, 0, s>>>(dy, f, z, offsets, E, rows, N, act, sr, cb, dz, part);
+        <<<grid, block, 0, s>>>(dy, f, z, rows, N, act, sr, cb, dz, part);
   };
   auto typed = [&](auto tag) {
     if (act == kActSwiglu) {

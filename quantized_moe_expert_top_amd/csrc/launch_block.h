@@ -38,9 +38,10 @@ size_t mm_backward_parts(int rows, int E, int N, int K);
 hipError_t launch_mm_pair(const MMArgs& nn, const MMArgs& tn, const PartSum& sum, int pair,
                           bool fp16, hipStream_t s, bool check);
 
-// dz = act'(z) dy (dz may be NULL), and column sums of dz over strips of rows
-// (part [dz_strips(rows, N, act)][N], may be NULL). offsets NULL: all rows; otherwise
-// rows [offsets[0], offsets[E]). part_f32: the sums' result is float32.
+// dz = act'(z) dy. part NULL: rows [offsets[0], offsets[E]), or all where offsets is
+// NULL. Otherwise all rows (offsets is not read), dz may be NULL, and part takes the
+// column sums of dz over strips of rows, [dz_strips(rows, N, act)][N]; part_f32: their
+// result is float32.
 int dz_strips(int rows, int N, int act);
 int dz_most_strips(int rows, int N, int act);   // of up to `rows` rows
 hipError_t launch_dz(const void* dy, bool dy_f32, const void* z, const int* offsets, int E,
