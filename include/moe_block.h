@@ -42,7 +42,10 @@ extern "C" {
 
 /* Activations of a product's output z. Every one but SWIGLU is element-wise.
  * SWIGLU takes z of width N (a multiple of 16) to N/2:
- * y_i = silu(z_i) * z_(N/2 + i), the W13 layout of moe.h. */
+ * y_i = silu(z_i) * z_(N/2 + i), the W13 layout of moe.h. Float32 results are
+ * within 18 * 2^-24 of the activation's value in its tails too (silu to z = -87, gelu
+ * to -13, 0 below). At an infinite z the formulas' 0 * infinity is NaN: silu and gelu
+ * of -infinity, their derivatives at both. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_SILU 2
@@ -107,8 +110,12 @@ MOE_API moe_status moe_grouped_mm(const moe_mm_shape* shape, const void* x, cons
  *   dw  dw_dtype (dtype or MOE_F32) [E, N, K] or NULL; every element is
  *       written (zero for an expert without rows)
  * dz is rounded to dtype where it enters the products (they run on dtype
- * operands); for MOE_ACT_NONE it is dy, unrounded. `ws` must hold
- * moe_grouped_mm_backward_workspace(shape) bytes (may be NULL when that is 0).
+ * operands); for MOE_ACT_NONE it is dy, unrounded. That rounding is one more of
+ * dtype's half steps in dx and dw, and in MOE_FP16 it takes a dz under 2^-25 to zero
+ * and one of 65520 or more to infinity, even where its factors (SwiGLU: dy, up and
+ * silu') are in range: scale the loss for MOE_FP16, as for any gradient in that type.
+ * `ws` must hold moe_grouped_mm_backward_workspace(shape) bytes (may be NULL when
+ * that is 0).
  */
 MOE_API size_t moe_grouped_mm_backward_workspace(const moe_mm_shape* shape);
 MOE_API moe_status moe_grouped_mm_backward(const moe_mm_shape* shape, const void* dy,
@@ -141,10 +148,12 @@ MOE_API moe_status moe_linear(const moe_mm_shape* shape, const void* x, const vo
  *   dx     dx_dtype (dtype or MOE_F32) [rows, K] or NULL
  *   dw     dw_dtype (dtype or MOE_F32) [N, K] or NULL
  *   dbias  dw_dtype [N] or NULL
- * dz is rounded to dtype where it enters the products, not in dbias. With
- * rows = 0, dw and dbias are set to zero. `ws` must hold
+ * dz is rounded to dtype where it enters the products (as in
+ * moe_grouped_mm_backward: in MOE_FP16 a float32 dy does not widen its range), not
+ * in dbias. With rows = 0, dw and dbias are set to zero. `ws` must hold
  * moe_linear_backward_workspace(shape) bytes, which grow with rows: a workspace
- * for the most rows serves fewer.
+ * for the most rows serves fewer. They count a dz of rows * N values always: the
+ * shape does not say whether dy itself is dz (MOE_ACT_NONE, dy of dtype).
  */
 MOE_API size_t moe_linear_backward_workspace(const moe_mm_shape* shape);
 MOE_API moe_status moe_linear_backward(const moe_mm_shape* shape, const void* dy,
@@ -204,7 +213,8 @@ typedef struct {
  *   n     = y * w_post / sqrt(mean(y^2) + eps)      (n = y where w_post is NULL)
  *   r_out = r + scale * gate * n                    (r_out = r where y is NULL)
  *   h     = r_out * w_pre / sqrt(mean(r_out^2) + eps)
- * h is computed from r_out before it is rounded.
+ * h is computed from r_out before it is rounded. The mean squares are float32: a row
+ * whose squares sum to 2^128 or more (values of about 1e19) has an infinite one.
  *   y       y_dtype [T, H] or NULL (then w_post, gate and r_out must be NULL)
  *   r       r_dtype [T, H]
  *   r_out   r_dtype [T, H], written where y is given (may be NULL)

@@ -139,7 +139,8 @@ def grouped_mm_backward(dy, x, w, expert_offsets, dx=None, dw=None, sorted_slot=
     dw [E, N, K], each of x's type or float32 and either of them None; dy
     [rows, N or N / 2] of x's type, z the forward's (act="none": None). Every
     element of dw is written; rows of dx outside the experts' blocks stay as
-    they were. ws: grouped_mm_backward_workspace bytes."""
+    they were. act'(z) dy enters the products in x's type: for float16 under 2^-25 it
+    is zero, from 65520 on infinite. ws: grouped_mm_backward_workspace bytes."""
     args = (dy, x, w, z, expert_offsets, sorted_slot, dx, dw, ws, topk, _act(act), stream)
     st = (_binding or _ext()).grouped_mm_backward(*args)
     if st:
@@ -168,7 +169,9 @@ def linear_backward(dy, x, w, dx=None, dw=None, dbias=None, act: str = "none", z
     """Gradients of linear: dx [rows, K], dw [N, K], dbias [N], each of x's type
     or float32 (dw and dbias alike), any of them None; dy [rows, N or N / 2] of
     x's type or float32, z the forward's (act="none": None). The residual's
-    gradient is dy. ws: linear_backward_workspace bytes."""
+    gradient is dy. act'(z) dy enters dx and dw in x's type, float32 dy or not: for
+    float16 under 2^-25 it is zero, from 65520 on infinite. ws:
+    linear_backward_workspace bytes."""
     args = (dy, x, w, z, dx, dw, dbias, ws, _act(act), stream)
     st = (_binding or _ext()).linear_backward(*args)
     if st:

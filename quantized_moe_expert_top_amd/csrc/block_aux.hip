@@ -35,6 +35,10 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float (&v)[8]) 
 // bias gradient is float32.
 constexpr int kDzCols = 512;
 
+// dz is stored in the operands' type: the matrix instructions take 16-bit operands,
+// and two parts of it would double both products. Its half step adds to that of the
+// results (relative 2-norm of dx and dW: bf16 0.00166 with a float32 dz, 0.00235;
+// fp16 0.00021, 0.00029); the bias sums take it unrounded.
 template <class T, bool SWIGLU, bool EXACT>
 __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, int dy_f32,
                                                  const void* __restrict__ z,

@@ -179,3 +179,31 @@ def test_gradient_error_is_relative_to_the_result(act, t):
             tol = torch.cat(((tol + U * (d * a).abs()) * u.abs(), 9.2 * U * (d * s).abs()))
     err = ((db.double() - want).abs() / (tol + 2.0 ** -149)).max().item()
     assert err <= 1.0, f"error {err:.3g} times its bound"
+
+
+@pytest.mark.parametrize("t", [BF, HF])
+def test_range_of_dz(t):
+    """A float32 dy enters dx and dw rounded to the operands' type, with its range (in
+    fp16 under 2^-25 zero, from 65520 on infinite; both ends of the range exact), and the
+    bias gradient as it is."""
+    import quantized_moe_expert_top_amd as moe
+    values = [2.0 ** -24, 2.0 ** -26, 65504.0, 65520.0, 2.0 ** 100, 2.0 ** -100, 0.0, 1.0]
+    N = K = 16
+    _say("range of dz", t)
+    dy = torch.tensor(values, device="cuda").view(-1, 1).repeat(1, N)
+    rows = dy.shape[0]
+    w = torch.zeros((N, K), dtype=t, device="cuda")
+    w[0, 0] = 1          # dx[:, 0] = dz[:, 0] + 0 dz[:, 1] + ..., NaN where dz is infinite
+    x = torch.zeros((rows, K), dtype=t, device="cuda")
+    dx = torch.empty((rows, K), dtype=F32, device="cuda")
+    db = torch.empty((N,), dtype=F32, device="cuda")
+    ws = torch.empty(moe.linear_backward_workspace(rows, K, N), dtype=torch.uint8, device="cuda")
+    moe.linear_backward(dy, x, w, dx=dx, dbias=db, ws=ws)
+    torch.cuda.synchronize()
+    want = (dy.to(t).float() * w[:, 0].float()).sum(1)
+    assert torch.equal(dx[:, 0].nan_to_num(nan=-1.0), want.nan_to_num(nan=-1.0))
+    if t == HF:
+        assert dx[1, 0] == 0 and dx[2, 0] == 65504 and dx[0, 0] == 2.0 ** -24
+        assert torch.isnan(dx[3:5, 0]).all()
+    # the sum of the eight values is 2^100 to float32's half step and seven roundings
+    assert abs(db.double() - sum(values)).max() <= 8 * 2.0 ** -24 * sum(values)
