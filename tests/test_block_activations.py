@@ -207,3 +207,81 @@ def test_range_of_dz(t):
         assert torch.isnan(dx[3:5, 0]).all()
     # the sum of the eight values is 2^100 to float32's half step and seven roundings
     assert abs(db.double() - sum(values)).max() <= 8 * 2.0 ** -24 * sum(values)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("t", [BF, HF])
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+def test_half_results_are_one_rounding_off(act, t, rows):
+    """16-bit results: one rounding to them, and an exponential whose argument a is
+    rounded (|a| U of the result: |z| for silu, twice z^2 / 2 for gelu)."""
+    import quantized_moe_expert_top_amd as moe
+    No, K = 4096, 8
+    _say("half activation", act, t, rows)
+    z = arguments(*RANGE[act], No).to(t).double().clamp(*RANGE[act]).cuda()
+    N = 2 * No if act == "swiglu" else No
+    w = torch.zeros((N, K), dtype=t, device="cuda")
+    w[:No, 0] = z.to(t)
+    w[No:, 0] = 1
+    x = torch.zeros((rows, K), dtype=t, device="cuda")
+    x[:, 0] = 1
+    y = torch.empty((rows, No), dtype=t, device="cuda")
+    moe.linear(x, w, y, act=act)
+    torch.cuda.synchronize()
+    z = w[:No, 0].double()
+    want = z * cdf64(z) if act == "gelu" else silu64(z)
+    a = z * z if act == "gelu" else z.abs()
+    tiny = 2.0 ** -25 if t == HF else 2.0 ** -134
+    tol = (torch.finfo(t).eps / 2 + (18 + a) * U * (1 + 2.0 ** -8)) * want.abs() + tiny
+    err = ((y.double() - want).abs() / tol).max().item()
+    assert err <= 1.0, f"error {err:.3g} times its bound"
+
+
+@pytest.mark.parametrize("ty", [BF, F32])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+def test_activations_of_infinities_and_nan(act, ty):
+    """What the formulas give in IEEE arithmetic: +infinity stays, silu and gelu of
+    -infinity and their derivatives at both infinities are 0 times infinity; a NaN stays,
+    and the neighbours of all of them are what they are without."""
+    import quantized_moe_expert_top_amd as moe
+    inf, nan = float("inf"), float("nan")
+    zs = [1.5, inf, -inf, nan, -2.0, 0.0, -0.0, 3e38]
+    K, No = 8, 8
+    _say("infinities", act, ty)
+    N = 16 if act == "swiglu" else 8
+    w = torch.zeros((N, K), dtype=BF, device="cuda")
+    w[:, 0] = 1
+    w[:8, 0] = torch.tensor(zs)
+    x = torch.zeros((3, K), dtype=BF, device="cuda")
+    x[:, 0] = 1
+    y = torch.empty((3, No), dtype=ty, device="cuda")
+    moe.linear(x, w, y, act=act)
+    zt = torch.tensor(zs, dtype=torch.float64)
+    zt = zt.to(BF).double()
+    want = {"relu": zt.clamp(min=0), "gelu": zt * cdf64(zt)}.get(act, silu64(zt))
+    got = y.double().cpu()
+    tol = (2.0 ** -8 if ty == BF else 40 * U)
+    for row in got:
+        for g, v, z in zip(row.tolist(), want.tolist(), zs):
+            if act != "relu" and z == -inf:
+                assert g != g, (z, g)
+            elif v != v or abs(v) == inf:
+                assert str(g) == str(v), (z, g, v)
+            else:
+                assert abs(g - v) <= tol * abs(v), (z, g, v)
+    # derivatives, by the bias gradient of one row
+    zz = torch.ones((1, N), dtype=BF, device="cuda")
+    zz[0, :8] = torch.tensor(zs)
+    db = torch.empty((N,), dtype=ty, device="cuda")
+    ws = torch.empty(moe.linear_backward_workspace(1, K, N, act), dtype=torch.uint8, device="cuda")
+    moe.linear_backward(torch.ones((1, No), dtype=BF, device="cuda"), x[:1], w, dbias=db, act=act,
+                        z=zz, ws=ws)
+    torch.cuda.synchronize()
+    s = 1 / (1 + torch.exp(-zt))
+    want = {"relu": torch.where(zt > 0, 1.0, torch.where(zt.isnan(), zt, 0.0)),
+            "gelu": gelu_grad64(zt)[0]}.get(act, s * (1 + zt / (1 + torch.exp(zt))))
+    for g, v, z in zip(db[:8].double().tolist(), want.tolist(), zs):
+        if z != z or (act != "relu" and abs(z) == inf):
+            assert g != g, (z, g)
+        else:
+            assert abs(g - v) <= tol * max(abs(v), 1.0), (z, g, v)
