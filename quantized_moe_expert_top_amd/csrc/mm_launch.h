@@ -13,10 +13,11 @@ using MMWide = MMGeom<64, 128, 2, 4, 64, 3, 4>;    // 8 waves, two blocks per CU
 using MMSmall = MMGeom<64, 64, 2, 2, 64, 4, 2>;    // 4 waves, two blocks per CU
 // 4 waves, two blocks per CU: one block's loads and epilogue stand behind the
 // other's multiplies. Its 32-k stages read half cache lines of a K-major operand,
-// so a long K goes to Big (8192 x 4096 x 7168: 447 us expected against 376); with
-// few stages it wins (128 experts, 32768 rows x 2048 x 768 to float32: 215 against
-// 240 us; its row gradient 150 against 167). Waves of 128 x 64 (of 64 x 128: 223
-// against 217, row gradients of 1536 columns 283 against 277).
+// so a long K goes to Big (8192 x 4096 x 7168: 447 us expected against 376). With few
+// stages it is level or ahead (routed rows of 128 experts, 8 to 1513 of 32768 each:
+// 2048 x 768 to float32 225 us, Big 226; its row gradient 164, Big 171; row gradient
+// of 1536 x 2048 288, Big 297; behind where every expert has 256: 253, Big 233, which
+// the host cannot see). Waves of 128 x 64 (of 64 x 128: 226 and 291 for 225 and 288).
 using MMLong = MMGeom<128, 256, 1, 4, 32, 3, 2>;
 // 8 waves, one block per CU, four stages: where a dense product has too few tiles
 // for two blocks per CU a block alone has to keep enough loads in flight (1219 x 1728
@@ -27,7 +28,8 @@ using MMDeep = MMGeom<128, 128, 2, 4, 64, 4, 2>;
 // `s1`, `s2` or `s3` per 64-k stage with 64, 256 or `slots` blocks at work (fewer
 // blocks, more of the caches' rate for each), and `full` (a full round with experts'
 // weights from memory; `dense` without) or `part` (the last round) for first loads
-// and epilogues. Fitted; what the fit says and, in brackets, what was timed:
+// and epilogues. Fitted; what the fit says and, in brackets, what was timed
+// (cards differ by up to 7%):
 //   NT  8192 x 4096 x 7168   Big 395 (376)   Mid 460 (462)
 //       4096 x 2048 x 1536   Big 40 (44)     Mid 31 (31)    Wide 36 (35)    Small 45 (42)
 //       6115 x 5728 x 176    Big 46 (51)     Mid 46 (42)    Wide 39 (34)    Small 53 (51)
