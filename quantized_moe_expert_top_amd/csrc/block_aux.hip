@@ -31,8 +31,9 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float (&v)[8]) 
 
 // A block takes 512 columns of dy (8 per thread) and a strip of rows, four at a
 // time; bound by the bytes of dy, z and dz. The column sums stay in registers
-// over the strip and are joined in LDS in a fixed order. EXACT (see mm.h): where the
-// bias gradient is float32.
+// over the strip and are joined in LDS in a fixed order. EXACT (see mm.h): the sums,
+// where the bias gradient is float32; dz is the other form's always, so that dx and dw
+// are the same bits whether a bias gradient is asked for or not.
 constexpr int kDzCols = 512;
 
 // dz is stored in the operands' type: the matrix instructions take 16-bit operands,
@@ -62,30 +63,38 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* __restrict__ dy, in
   if (col < No) {
 #pragma unroll 2
     for (long long r = r0 + ty; r < r1; r += 4) {
-      float d[8], g[8];
+      float d[8], g[8], e[8], du[8], eu[8];   // dz; EXACT: e, what the sums take
       load8<T>(dy, r * No + col, dy_f32, d);
       if (SWIGLU) {
-        float u[8], du[8];
+        float u[8];
         load8<T>(z, r * N + col, false, g);
         load8<T>(z, r * N + No + col, false, u);
+        if (EXACT)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) swiglu_grad_f32<EXACT>(d[i], g[i], u[i], d[i], du[i]);
+          for (int i = 0; i < 8; ++i) swiglu_grad_f32<true>(d[i], g[i], u[i], e[i], eu[i]);
+        if (!EXACT || dz)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) swiglu_grad_f32<false>(d[i], g[i], u[i], d[i], du[i]);
         if (dz) {
           store8<T>(dz, r * N + col, d);
           store8<T>(dz, r * N + No + col, du);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[S - 1][i] += du[i];
+        for (int i = 0; i < 8; ++i) sum[S - 1][i] += EXACT ? eu[i] : du[i];
       } else {
-        if (act != 0) {
+        if (act != 0) {   // EXACT: it is not 0
           load8<T>(z, r * N + col, false, g);
+          if (EXACT)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] *= act_grad_f32<EXACT>(g[i], act);
+            for (int i = 0; i < 8; ++i) e[i] = d[i] * act_grad_f32<true>(g[i], act);
+          if (!EXACT || dz)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= act_grad_f32<false>(g[i], act);
         }
         if (dz) store8<T>(dz, r * N + col, d);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0][i] += d[i];
+      for (int i = 0; i < 8; ++i) sum[0][i] += EXACT ? e[i] : d[i];
     }
   }
   if (ty > 0)

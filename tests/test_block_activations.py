@@ -285,3 +285,30 @@ def test_activations_of_infinities_and_nan(act, ty):
             assert g != g, (z, g)
         else:
             assert abs(g - v) <= tol * max(abs(v), 1.0), (z, g, v)
+
+
+@pytest.mark.parametrize("tb", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+def test_a_bias_gradient_leaves_the_other_gradients_bits(act, tb):
+    """dx and dw are the same bits with a bias gradient of either type and without."""
+    import quantized_moe_expert_top_amd as moe
+    rows, K, N, t = 2051, 72, 1040, BF
+    _say("bits beside a bias gradient", act, tb)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(t)
+
+    No = N // 2 if act == "swiglu" else N
+    x, w, dy, z = rand(rows, K), rand(N, K), rand(rows, No), 3 * rand(rows, N)
+    ws = torch.empty(moe.linear_backward_workspace(rows, K, N, act), dtype=torch.uint8, device="cuda")
+    db = torch.empty((N,), dtype=tb, device="cuda")
+    got = []
+    for with_db in (False, True):
+        dx = torch.empty((rows, K), dtype=F32, device="cuda")
+        dw = torch.empty((N, K), dtype=tb, device="cuda")
+        moe.linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db if with_db else None, act=act, z=z, ws=ws)
+        torch.cuda.synchronize()
+        got.append((dx, dw))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
