@@ -11,6 +11,8 @@
  *   moe_block_norm      r' = r + scale * gate * rms(y; w_post), h = rms(r'; w_pre)
  *                       (the norms after one block and before the next, fused
  *                       with the residual stream), and its gradients
+ *   moe_layer_norm      r' = r + y, h = (r' - mean) / sqrt(var + eps) * w + b (the same
+ *                       place, for blocks with layer norms), and its gradients
  *   moe_combine_backward  the gradients of moe_combine and of moe_route_topk's
  *                       softmax over the picks
  *
@@ -249,6 +251,51 @@ MOE_API moe_status moe_block_norm_backward(const moe_norm_shape* shape, const vo
                                            const void* w_pre, void* dr, void* dy, float* dw_post,
                                            float* dw_pre, void* dgate, void* ws, size_t ws_bytes,
                                            void* stream);
+
+/*
+ * Shape of a layer norm: T, H, the types and eps as in moe_norm_shape.
+ */
+typedef struct {
+  int32_t T;
+  int32_t H;
+  int32_t dtype;   /* h, w, b */
+  int32_t r_dtype; /* r, r_out: dtype or MOE_F32 */
+  int32_t y_dtype; /* dtype or MOE_F32 */
+  float eps;
+} moe_layer_norm_shape;
+
+/*
+ * moe_layer_norm — a block's output added to the residual stream, and the layer norm
+ * before the next block, in one pass:
+ *   r_out = r + y                                    (r_out = r where y is NULL)
+ *   h     = (r_out - m) / sqrt(mean((r_out - m)^2) + eps) * w + b,  m = mean(r_out)
+ * h is computed from r_out before it is rounded; mean and variance are float32, the
+ * variance of what is left after the mean is taken off.
+ *   y       y_dtype [T, H] or NULL (then r_out must be NULL)
+ *   r       r_dtype [T, H]
+ *   r_out   r_dtype [T, H], written where y is given (may be NULL)
+ *   h       dtype [T, H];  w  dtype [H];  b  dtype [H] or NULL
+ */
+MOE_API moe_status moe_layer_norm(const moe_layer_norm_shape* shape, const void* r, const void* y,
+                                  const void* w, const void* b, void* r_out, void* h,
+                                  void* stream);
+
+/*
+ * moe_layer_norm_backward — the gradients of moe_layer_norm.
+ *   r_out   r_dtype [T, H]: the forward's (r itself where y was NULL)
+ *   dr_out  r_dtype [T, H] or NULL: the gradient that reaches r_out directly
+ *   dh      dtype [T, H];  w  dtype [H]
+ *   dr      r_dtype [T, H]: dr_out + the gradient through h (y's gradient too)
+ *   dw, db  float32 [H] or NULL (zeros where T is 0)
+ * Sums over tokens run in a fixed order. `ws` must hold
+ * moe_layer_norm_backward_workspace(T, H) bytes (used for dw and db; may be NULL where
+ * neither is asked for).
+ */
+MOE_API size_t moe_layer_norm_backward_workspace(int32_t T, int32_t H);
+MOE_API moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void* r_out,
+                                           const void* dr_out, const void* dh, const void* w,
+                                           void* dr, float* dw, float* db, void* ws,
+                                           size_t ws_bytes, void* stream);
 
 /*
  * moe_combine_backward — the gradients of out[t] = sum_j w[t, j] y[slot_pos[t*k + j]]

@@ -1,0 +1,117 @@
+/*
+ * moe_int8.h — C ABI of libmoe, third part: a block served in 8-bit integers on AMD
+ * Instinct MI355X (gfx950), around and with the W8A8 experts of moe.h.
+ *
+ *   moe_quant_rows   token rows to int8 codes with a scale per token
+ *   moe_linear_w8a8  y = act(x W^T + bias) + residual on int8 codes with scales per
+ *                    token and per output channel (shared experts, projections)
+ *   moe_layer_w8a8   the whole routed W8A8 layer in one call
+ *
+ * The conventions of moe.h hold for every call: device pointers to row-major
+ * contiguous arrays, 16-byte aligned; arguments checked on the host before anything is
+ * enqueued; no allocation, no synchronization, no pointer kept past the call; outputs
+ * must not alias inputs (but a residual may be the output itself); calls on distinct
+ * streams with distinct workspaces may run concurrently; two runs on the same inputs
+ * give identical bits. A workspace holds nothing between calls.
+ *
+ * Codes of a row (the rule of moe_grouped_w8a8_ffn): s = max|x| / 127 in float32 (IEEE
+ * division), q = x / s to the nearest whole number, ties to even, clamped to
+ * [-127, 127]; s = 0 and q = 0 for a row of zeros. A row that holds an infinity or a
+ * NaN gets s = NaN and q = 0: all that is computed from it is NaN, and other rows are
+ * not touched.
+ */
+#ifndef MOE_INT8_H
+#define MOE_INT8_H
+
+#include "moe.h"
+#include "moe_block.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MOE_INT8 3
+#define MOE_INT8_MAX_K 65536   /* largest K: sums of its products fit 32 bits */
+
+/*
+ * moe_quant_rows — int8 codes and scales of rows.
+ *   x      x_dtype (MOE_BF16, MOE_FP16 or MOE_F32) [rows, K]
+ *   q      int8 [rows, K];  scale  float32 [rows]
+ * Requires rows >= 0, K a positive multiple of 8, at most MOE_INT8_MAX_K.
+ */
+MOE_API moe_status moe_quant_rows(const void* x, int32_t x_dtype, int32_t rows, int32_t K,
+                                  int8_t* q, float* scale, void* stream);
+
+/*
+ * Shape of an int8 product. Let No = N/2 for MOE_ACT_SWIGLU and N otherwise.
+ *   rows     rows of y, at most 2^31 - 2^16; rows*max(N, K) <= 2^38
+ *   K        a multiple of 16, at most MOE_INT8_MAX_K
+ *   N        a multiple of 8 (of 16 for SWIGLU), at most 2^20; N*K <= 2^30
+ *   x_dtype  MOE_INT8 (codes, with x_scale), MOE_BF16 or MOE_FP16 (values: the call
+ *            makes their codes)
+ *   y_dtype  MOE_BF16, MOE_FP16 or MOE_F32
+ *   act      MOE_ACT_*
+ */
+typedef struct {
+  int32_t rows;
+  int32_t K;
+  int32_t N;
+  int32_t x_dtype;
+  int32_t y_dtype;
+  int32_t act;
+} moe_w8_shape;
+
+/*
+ * moe_linear_w8a8 — a dense product of int8 codes with its epilogue.
+ *   z[t, n] = (sum_k q[t, k] w[n, k]) * x_scale[t] * w_scale[n] + bias[n]
+ *   y = act(z) + residual
+ *   x         int8 [rows, K], or x_dtype [rows, K], whose codes (those of
+ *             moe_quant_rows) the call makes
+ *   x_scale   float32 [rows] with MOE_INT8, NULL otherwise
+ *   w         int8 [N, K];  w_scale  float32 [N]
+ *   bias      float32 [N] or NULL
+ *   residual  y_dtype [rows, No] or NULL; may be y itself (added in place)
+ *   y         y_dtype [rows, No]
+ * The sum is exact in 32 bits for every value of the codes; it is rounded to float32
+ * once and the rest is float32 with one rounding to y_dtype. `ws` must hold
+ * moe_linear_w8a8_workspace(rows, K) bytes where x holds values; with codes it is not
+ * used and may be NULL. The bytes grow with rows: a workspace for the most rows serves
+ * fewer.
+ */
+MOE_API size_t moe_linear_w8a8_workspace(int32_t rows, int32_t K);
+MOE_API moe_status moe_linear_w8a8(const moe_w8_shape* shape, const void* x, const float* x_scale,
+                                   const int8_t* w, const float* w_scale, const float* bias,
+                                   const void* residual, void* y, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * moe_layer_w8a8 — the whole W8A8 layer in one call: moe_route_topk's picks of
+ * logits [T, E], the SwiGLU experts of moe_grouped_w8a8_ffn, and moe_combine's sum
+ * added to a residual, by the definitions given there:
+ *   out[t] = residual[t] + sum_{j < k} topk_w[t, j] * y[t, j],
+ * summed in float32 in increasing j, the residual last, and rounded once to out_dtype.
+ *   logits    float32 [T, E]
+ *   x         x_dtype (MOE_BF16 or MOE_FP16) [T, H]
+ *   w13       int8 [E, 2I, H] (rows [0, I) gate, [I, 2I) up);  s13  float32 [E, 2I]
+ *   w2        int8 [E, H, I];  s2  float32 [E, H]
+ *   residual  out_dtype [T, H] or NULL; may be out itself
+ *   topk_ids  int32 [T, k];  topk_w  float32 [T, k]  (outputs)
+ *   expert_offsets  int32 [E + 1] or NULL (output, as moe_permute's; feeds
+ *             moe_expert_counts_accumulate)
+ *   out       out_dtype (MOE_BF16, MOE_FP16 or MOE_F32) [T, H]
+ * Requires what moe_grouped_w8a8_ffn does. `ws` must hold
+ * moe_layer_w8a8_workspace(shape) bytes.
+ */
+MOE_API size_t moe_layer_w8a8_workspace(const moe_shape* shape);
+MOE_API moe_status moe_layer_w8a8(const moe_shape* shape, const float* logits, const void* x,
+                                  int32_t x_dtype, const int8_t* w13, const float* s13,
+                                  const int8_t* w2, const float* s2, const void* residual,
+                                  int32_t* topk_ids, float* topk_w, int32_t* expert_offsets,
+                                  void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MOE_INT8_H */

@@ -19,7 +19,12 @@ from ._lib import (  # noqa: F401
 from ._block import (  # noqa: F401
     block_norm, block_norm_backward, block_norm_backward_workspace, combine_backward, grouped_mm,
     grouped_mm_backward, grouped_mm_backward_workspace, linear, linear_backward,
-    linear_backward_workspace, product_plan,
+    layer_norm, layer_norm_backward, layer_norm_backward_workspace, linear_backward_workspace,
+    product_plan,
+)
+
+from ._int8 import (  # noqa: F401
+    layer_w8a8, layer_w8a8_workspace, linear_w8a8, linear_w8a8_workspace, quant_rows,
 )
 
 __all__ = ["MoeError", "LayerBuffers", "moe_forward", "moe_layer", "load", "router_logits",
@@ -27,7 +32,8 @@ __all__ = ["MoeError", "LayerBuffers", "moe_forward", "moe_layer", "load", "rout
            "permute", "grouped_w4a16_ffn", "grouped_w4a8_ffn", "grouped_w8a8_ffn", "combine",
            "layer_w4a16", "layer_w4a16_noalloc", "expert_counts_accumulate", "expert_hot_rank",
            "grouped_mm", "grouped_mm_backward", "linear", "linear_backward", "block_norm",
-           "block_norm_backward", "combine_backward", "product_plan"]
+           "block_norm_backward", "combine_backward", "product_plan", "layer_norm",
+           "layer_norm_backward", "quant_rows", "linear_w8a8", "layer_w8a8"]
 
 
 @dataclass
@@ -60,7 +66,8 @@ class LayerBuffers:
         pws = _lib.permute_workspace(T, E, k)
         fws = {"w4a16": _lib.w4a16_workspace, "w4a8": _lib.w4a8_workspace,
                "w8a8": _lib.w8a8_workspace}[fmt](T, H, I, E, k)
-        lws = _lib.layer_w4a16_workspace(T, H, I, E, k) if fmt == "w4a16" else 0
+        lws = {"w4a16": _lib.layer_w4a16_workspace, "w8a8": layer_w8a8_workspace}.get(
+            fmt, lambda *_: 0)(T, H, I, E, k)
         return cls(
             T, H, I, E, k, fmt,
             ids=torch.empty((T, k), **i32),
@@ -100,11 +107,18 @@ def moe_forward(b: LayerBuffers, x, logits, weights, debug=None, stream=None):
 
 
 def moe_layer(b: LayerBuffers, x, logits, weights, stream=None):
-    """The same layer through the single whole-layer entry point
-    (moe_layer_w4a16; fused kernels at decode sizes). Returns b.out."""
-    if b.fmt != "w4a16":
-        raise ValueError("moe_layer covers the W4A16 format")
+    """The same layer through the single whole-layer entry point (moe_layer_w4a16 or
+    moe_layer_w8a8; fused kernels at decode sizes). Returns b.out. W8A8: of the buffers,
+    ids, w, offsets and out are written."""
+    if b.fmt not in ("w4a16", "w8a8"):
+        raise ValueError("moe_layer covers the W4A16 and W8A8 formats")
     w13, s13, w2, s2 = weights
+    if b.fmt == "w8a8":
+        import torch
+        x = x.view(torch.bfloat16) if x.dtype == torch.int16 else x   # bf16 bits
+        layer_w8a8(logits, x, w13, s13, w2, s2, b.ids, b.w, b.out, b.layer_ws,
+                   expert_offsets=b.offsets, stream=stream)
+        return b.out
     _lib.layer_w4a16((b.T, b.H, b.I, b.E, b.k), logits, x, w13, s13, w2, s2, b.ids, b.w,
                      b.offsets, b.sorted_slot, b.slot_pos, b.active, b.n_active, b.y, b.out,
                      b.layer_ws, stream)

@@ -19,7 +19,8 @@ from ._lib import _check
 EXPORTS = ("moe_grouped_mm", "moe_grouped_mm_backward_workspace", "moe_grouped_mm_backward",
            "moe_linear", "moe_linear_backward_workspace", "moe_linear_backward",
            "moe_block_norm", "moe_block_norm_backward_workspace", "moe_block_norm_backward",
-           "moe_combine_backward", "moe_product_plan")
+           "moe_combine_backward", "moe_product_plan", "moe_layer_norm",
+           "moe_layer_norm_backward_workspace", "moe_layer_norm_backward")
 
 BF16, FP16, F32 = 0, 1, 2
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
@@ -35,9 +36,19 @@ class MoeNormShape(ctypes.Structure):
                 [("scale", ctypes.c_float), ("eps", ctypes.c_float)])
 
 
+class MoeLayerNormShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "H", "dtype", "r_dtype", "y_dtype")] +
+                [("eps", ctypes.c_float)])
+
+
+class MoeW8Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "K", "N", "x_dtype", "y_dtype", "act")]
+
+
 BINDING_PATH = os.path.join(_lib.HERE, "_block_binding.so")
 _CALLS = ("moe_grouped_mm", "moe_grouped_mm_backward", "moe_linear", "moe_linear_backward",
-          "moe_block_norm", "moe_block_norm_backward", "moe_combine_backward")
+          "moe_block_norm", "moe_block_norm_backward", "moe_combine_backward", "moe_layer_norm",
+          "moe_layer_norm_backward", "moe_quant_rows", "moe_linear_w8a8", "moe_layer_w8a8")
 
 _declared = False
 _binding = None
@@ -49,6 +60,8 @@ def _load() -> ctypes.CDLL:
     if not _declared:
         P, I32, SZ, INT = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
         mm, norm = ctypes.POINTER(MoeMMShape), ctypes.POINTER(MoeNormShape)
+        ln, w8 = ctypes.POINTER(MoeLayerNormShape), ctypes.POINTER(MoeW8Shape)
+        layer = ctypes.POINTER(_lib.MoeShape)
         sig = {
             "moe_grouped_mm": (INT, [mm] + [P] * 6 + [I32, P]),
             "moe_grouped_mm_backward_workspace": (SZ, [mm]),
@@ -61,6 +74,14 @@ def _load() -> ctypes.CDLL:
             "moe_block_norm_backward": (INT, [norm] + [P] * 13 + [SZ, P]),
             "moe_product_plan": (INT, [mm, I32, P]),
             "moe_combine_backward": (INT, [P] * 5 + [I32] * 4 + [P, I32, P, P, P]),
+            "moe_layer_norm": (INT, [ln] + [P] * 7),
+            "moe_layer_norm_backward_workspace": (SZ, [I32, I32]),
+            "moe_layer_norm_backward": (INT, [ln] + [P] * 8 + [SZ, P]),
+            "moe_quant_rows": (INT, [P, I32, I32, I32, P, P, P]),
+            "moe_linear_w8a8_workspace": (SZ, [I32, I32]),
+            "moe_linear_w8a8": (INT, [w8] + [P] * 8 + [SZ, P]),
+            "moe_layer_w8a8_workspace": (SZ, [layer]),
+            "moe_layer_w8a8": (INT, [layer, P, P, I32] + [P] * 9 + [I32, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -241,3 +262,32 @@ def combine_backward(dout, y, slot_pos, topk_w, dy=None, dtopk_w=None, topk_ids=
     st = (_binding or _ext()).combine_backward(*args)
     if st:
         _done("moe_combine_backward", st, lambda: _binding.combine_backward(*args))
+
+
+def layer_norm(r, w, h, b=None, y=None, r_out=None, eps: float = 1e-5, stream=None) -> None:
+    """r_out = r + y; h = (r_out - mean) / sqrt(var + eps) * w + b.
+
+    r, r_out [T, H] and y [T, H] are float32 or the half type of the rest (w, b [H],
+    h [T, H]: bfloat16 or float16). y None: h of r itself, and no r_out. h is computed
+    from r_out before it is rounded."""
+    args = (r, y, w, b, r_out, h, eps, stream)
+    st = (_binding or _ext()).layer_norm(*args)
+    if st:
+        _done("moe_layer_norm", st, lambda: _binding.layer_norm(*args))
+
+
+def layer_norm_backward_workspace(T: int, H: int) -> int:
+    """Bytes of workspace layer_norm_backward needs for gradients of w and b."""
+    return int(_load().moe_layer_norm_backward_workspace(T, H))
+
+
+def layer_norm_backward(r_out, w, dh, dr, dr_out=None, dw=None, db=None, eps: float = 1e-5,
+                        ws=None, stream=None) -> None:
+    """Gradients of layer_norm from dh [T, H] and, where it is used further, dr_out
+    [T, H] (r_out's type). r_out is the forward's (r itself where y was None). dr like
+    r_out: r's gradient, and y's; dw, db float32 [H]. ws: layer_norm_backward_workspace
+    bytes, where dw or db is asked for."""
+    args = (r_out, dr_out, dh, w, dr, dw, db, ws, eps, stream)
+    st = (_binding or _ext()).layer_norm_backward(*args)
+    if st:
+        _done("moe_layer_norm_backward", st, lambda: _binding.layer_norm_backward(*args))

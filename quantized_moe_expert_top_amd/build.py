@@ -29,7 +29,8 @@ LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cpp", "router.hip", "route.hip", "permute.hip", "w4a16.hip", "w4a8.hip",
            "w8a8.hip", "combine.hip", "telemetry.hip",
            "block_api.cpp", "mm_nt.hip", "mm_nn.hip", "mm_tn.hip", "mm_pair.hip", "block_aux.hip", "norm.hip",
-           "combine_backward.hip"]
+           "layer_norm.hip", "combine_backward.hip",
+           "int8_api.cpp", "mm_i8.hip", "quant.hip", "layer_w8a8.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -58,16 +58,6 @@ moe_status launched(hipError_t err, const char* what) {
   return MOE_OK;
 }
 
-}  // namespace moe_api
-
-using moe_api::aligned16;
-using moe_api::check_device;
-using moe_api::fail;
-using moe_api::kMaxDevices;
-using moe_api::launched;
-
-namespace {
-
 moe_status check_route_dims(int32_t T, int32_t E, int32_t k) {
   if (T < 0) return fail(MOE_EINVAL, "T = %d < 0", T);
   if (E < 1 || E > MOE_MAX_EXPERTS) return fail(MOE_ESHAPE, "E = %d outside [1, %d]", E, MOE_MAX_EXPERTS);
@@ -95,6 +85,18 @@ moe_status check_shape(const moe_shape* s, int hmod, int imod) {
                 2LL * s->H * s->I);
   return MOE_OK;
 }
+
+}  // namespace moe_api
+
+using moe_api::aligned16;
+using moe_api::check_device;
+using moe_api::check_route_dims;
+using moe_api::check_shape;
+using moe_api::fail;
+using moe_api::kMaxDevices;
+using moe_api::launched;
+
+namespace {
 
 // Scratch of moe_layer_w4a16_noalloc: a file-scope device array, one copy per
 // GPU, held until the process ends. In host code the array's name is only a

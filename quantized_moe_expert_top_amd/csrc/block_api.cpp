@@ -12,16 +12,17 @@
 
 namespace {
 
+using moe_api::align256;
 using moe_api::check_device;
+using moe_api::check_overlap;
 using moe_api::fail;
 using moe_api::launched;
+using moe_api::values;
 
 constexpr int64_t kMaxFeatures = 1 << 20;    // K and N: 32-bit offsets inside a tile's rows
 constexpr int64_t kMaxResource = 1LL << 30;  // values behind one buffer resource (2 GiB)
 constexpr int32_t kMaxRows = INT32_MAX - 65535;   // room for the ends of tiles and splits
 constexpr int64_t kMaxValues = 1LL << 38;    // values of one array: bounds every grid
-
-size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 int out_width(const moe_mm_shape* s) { return s->act == MOE_ACT_SWIGLU ? s->N / 2 : s->N; }
 
@@ -65,30 +66,6 @@ moe_status check_gather(const moe_mm_shape* s, const int32_t* sorted_slot) {
     return fail(MOE_ESHAPE, "x_rows*K = %lld above 2^30",
                 static_cast<long long>(s->x_rows) * s->K);
   return MOE_OK;
-}
-
-// Arrays of a call: no output may overlap an input or another output.
-struct Span {
-  const char* name;
-  const void* p;
-  size_t bytes;
-  bool out;
-};
-template <int N>
-moe_status check_overlap(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i) {
-    if (!s[i].out || !s[i].p || !s[i].bytes) continue;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), b = a + s[i].bytes;
-    for (int j = 0; j < N; ++j) {
-      if (j == i || (s[j].out && j < i) || !s[j].p || !s[j].bytes) continue;
-      const uintptr_t c = reinterpret_cast<uintptr_t>(s[j].p), d = c + s[j].bytes;
-      if (a < d && c < b) return fail(MOE_EINVAL, "%s overlaps %s in memory", s[i].name, s[j].name);
-    }
-  }
-  return MOE_OK;
-}
-size_t values(int64_t rows, int64_t cols, int type) {
-  return static_cast<size_t>(rows) * cols * (type == MOE_F32 ? 4 : 2);
 }
 
 moe::MMArgs mm_args(const moe_mm_shape* s, const int32_t* offsets, const int32_t* slot) {
@@ -561,6 +538,104 @@ moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* r_ou
   return launched(moe::launch_block_norm_backward(a, shape->dtype == MOE_FP16, dw_pre, dw_post,
                                                   dg_channel, static_cast<hipStream_t>(stream)),
                   "moe_block_norm_backward launch");
+}
+
+static moe_status check_layer_norm(const moe_layer_norm_shape* s) {
+  if (!s) return fail(MOE_EINVAL, "shape is NULL");
+  const moe_norm_shape n = {s->T, s->H, s->dtype, s->r_dtype, s->y_dtype, MOE_GATE_NONE, 1.0f, s->eps};
+  return check_norm(&n);
+}
+
+moe_status moe_layer_norm(const moe_layer_norm_shape* shape, const void* r, const void* y,
+                          const void* w, const void* b, void* r_out, void* h, void* stream) {
+  moe_status st = check_layer_norm(shape);
+  if (st) return st;
+  if (!y && r_out) return fail(MOE_EINVAL, "r_out needs y");
+  if (shape->T == 0) return MOE_OK;
+  REQUIRE_PTR(r);
+  if (y) REQUIRE_PTR(y);
+  REQUIRE_PTR(w);
+  if (b) REQUIRE_PTR(b);
+  if (r_out) REQUIRE_PTR(r_out);
+  REQUIRE_PTR(h);
+  const int64_t T = shape->T, H = shape->H;
+  const int t = shape->dtype;
+  if ((st = check_overlap({{"r_out", r_out, values(T, H, shape->r_dtype), true},
+                           {"h", h, values(T, H, t), true},
+                           {"r", r, values(T, H, shape->r_dtype), false},
+                           {"y", y, values(T, H, shape->y_dtype), false},
+                           {"w", w, values(1, H, t), false},
+                           {"b", b, values(1, H, t), false}})))
+    return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::LayerNormArgs a = {};
+  a.r = r;
+  a.y = y;
+  a.w = w;
+  a.b = b;
+  a.r_out = r_out;
+  a.h = h;
+  a.T = shape->T;
+  a.H = shape->H;
+  a.r_f32 = shape->r_dtype == MOE_F32;
+  a.y_f32 = shape->y_dtype == MOE_F32;
+  a.eps = shape->eps;
+  return launched(moe::launch_layer_norm(a, t == MOE_FP16, static_cast<hipStream_t>(stream)),
+                  "moe_layer_norm launch");
+}
+
+size_t moe_layer_norm_backward_workspace(int32_t T, int32_t H) {
+  if (T < 0 || H < 8 || H % 8 || H > MOE_NORM_MAX_H) return 0;
+  return align256(static_cast<size_t>(moe::layer_norm_backward_blocks(T, H)) * 2 * H * 4);
+}
+
+moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void* r_out,
+                                   const void* dr_out, const void* dh, const void* w, void* dr,
+                                   float* dw, float* db, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_layer_norm(shape);
+  if (st) return st;
+  const bool sums = dw || db;
+  if (shape->T == 0 && !sums) return MOE_OK;
+  if (dw) REQUIRE_PTR(dw);
+  if (db) REQUIRE_PTR(db);
+  if (shape->T > 0) {
+    REQUIRE_PTR(r_out);
+    if (dr_out) REQUIRE_PTR(dr_out);
+    REQUIRE_PTR(dh);
+    REQUIRE_PTR(w);
+    REQUIRE_PTR(dr);
+  }
+  const size_t need = moe_layer_norm_backward_workspace(shape->T, shape->H);
+  if (sums && need > 0) {
+    if (ws_bytes < need)
+      return fail(MOE_EWORKSPACE, "layer norm backward workspace %zu < %zu bytes", ws_bytes, need);
+    REQUIRE_PTR(ws);
+  }
+  const int64_t T = shape->T, H = shape->H;
+  if ((st = check_overlap({{"dr", dr, values(T, H, shape->r_dtype), true},
+                           {"dw", dw, values(1, H, MOE_F32), true},
+                           {"db", db, values(1, H, MOE_F32), true},
+                           {"ws", sums ? ws : nullptr, need, true},
+                           {"r_out", r_out, values(T, H, shape->r_dtype), false},
+                           {"dr_out", dr_out, values(T, H, shape->r_dtype), false},
+                           {"dh", dh, values(T, H, shape->dtype), false},
+                           {"w", w, values(1, H, shape->dtype), false}})))
+    return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::LayerNormArgs a = {};
+  a.r = r_out;
+  a.dr_out = dr_out;
+  a.dh = dh;
+  a.w = w;
+  a.dr = dr;
+  a.part = sums ? static_cast<float*>(ws) : nullptr;
+  a.T = shape->T;
+  a.H = shape->H;
+  a.r_f32 = shape->r_dtype == MOE_F32;
+  a.eps = shape->eps;
+  return launched(moe::launch_layer_norm_backward(a, shape->dtype == MOE_FP16, dw, db,
+                                                  static_cast<hipStream_t>(stream)),
+                  "moe_layer_norm_backward launch");
 }
 
 moe_status moe_combine_backward(const float* dout, const float* y, const int32_t* slot_pos,

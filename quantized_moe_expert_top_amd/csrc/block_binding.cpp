@@ -1,8 +1,8 @@
-// CPython binding of the block operators (moe_block.h): checks the tensors of a
+// CPython binding of the block operators and the int8 ones (moe_block.h, moe_int8.h): checks the tensors of a
 // call and passes their addresses on. A call of a few microseconds on the GPU costs
 // more in Python attribute lookups (shape, type, layout, device, address of up to
-// 13 tensors) than on the device, so the checks are made here; _block.py holds the
-// entry points with their defaults and documentation.
+// 13 tensors) than on the device, so the checks are made here; _block.py and _int8.py
+// hold the entry points with their defaults and documentation.
 //
 // Every function takes its tensors (or None), its scalars and the stream (an
 // integer, or None for the current stream of the tensors' GPU), and returns the
@@ -16,7 +16,7 @@
 #include <initializer_list>
 #include <string>
 
-#include "../../include/moe_block.h"
+#include "../../include/moe_int8.h"
 
 namespace {
 
@@ -28,6 +28,11 @@ decltype(&moe_linear_backward) f_linear_backward;
 decltype(&moe_block_norm) f_block_norm;
 decltype(&moe_block_norm_backward) f_block_norm_backward;
 decltype(&moe_combine_backward) f_combine_backward;
+decltype(&moe_layer_norm) f_layer_norm;
+decltype(&moe_layer_norm_backward) f_layer_norm_backward;
+decltype(&moe_quant_rows) f_quant_rows;
+decltype(&moe_linear_w8a8) f_linear_w8a8;
+decltype(&moe_layer_w8a8) f_layer_w8a8;
 PyObject* g_get_device = nullptr;   // () -> current device
 PyObject* g_get_stream = nullptr;   // (device) -> current raw stream
 bool g_has_gpu = false;
@@ -47,9 +52,11 @@ std::string shape_text(c10::IntArrayRef s) {
 
 using at::ScalarType;
 constexpr ScalarType kBf = ScalarType::BFloat16, kHf = ScalarType::Half, kF32 = ScalarType::Float,
-                     kI32 = ScalarType::Int;
+                     kI32 = ScalarType::Int, kI8 = ScalarType::Char;
 
-int type_code(ScalarType t) { return t == kBf ? MOE_BF16 : t == kHf ? MOE_FP16 : MOE_F32; }
+int type_code(ScalarType t) {
+  return t == kBf ? MOE_BF16 : t == kHf ? MOE_FP16 : t == kI8 ? MOE_INT8 : MOE_F32;
+}
 
 // The operands of one call: the tensors are borrowed from the argument array.
 class Call {
@@ -195,6 +202,21 @@ void gather_shape(moe_mm_shape& s, const at::Tensor& x, const at::Tensor& offset
     refuse("x has " + std::to_string(x.size(0)) + " rows, the call needs " +
            std::to_string(s.rows));
   }
+}
+
+// r [T, H], weights of one half type
+moe_layer_norm_shape layer_norm_shape(const at::Tensor& r, const at::Tensor* y, const at::Tensor& w,
+                                      double eps) {
+  if (r.dim() != 2)
+    refuse("the residual stream has shape " + shape_text(r.sizes()) + "; [T, H] is needed");
+  moe_layer_norm_shape s = {};
+  s.T = dim32(r.size(0), "T");
+  s.H = dim32(r.size(1), "H");
+  s.dtype = type_code(half_of(w, "w"));
+  s.r_dtype = type_code(r.scalar_type());
+  s.y_dtype = y ? type_code(y->scalar_type()) : s.dtype;
+  s.eps = static_cast<float>(eps);
+  return s;
 }
 
 template <class F>
@@ -452,30 +474,178 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(addresses of the seven entry points in the order above, get_device,
-// get_stream, has_gpu)
+// r, y, w, b, r_out, h, eps, stream
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guard([&]() -> PyObject* {
+    Call c(a, n, 8, "layer_norm");
+    const at::Tensor& r = c.need(0, "r");
+    const at::Tensor* y = c.tensor(1, "y");
+    const at::Tensor& w = c.need(2, "w");
+    const at::Tensor *b = c.tensor(3, "b"), *ro = c.tensor(4, "r_out");
+    const at::Tensor& h = c.need(5, "h");
+    const moe_layer_norm_shape s = layer_norm_shape(r, y, w, c.number(6));
+    const ScalarType t = w.scalar_type();
+    want(&r, "r", {s.T, s.H}, {t, kF32});
+    want(y, "y", {s.T, s.H}, {t, kF32});
+    want(&w, "w", {s.H}, {t});
+    want(b, "b", {s.H}, {t});
+    want(ro, "r_out", {s.T, s.H}, {r.scalar_type()});
+    want(&h, "h", {s.T, s.H}, {t});
+    void* st;
+    if (!c.stream(7, &st)) return other_device(c);
+    return run(f_layer_norm, &s, ptr(r), ptr(y), ptr(w), ptr(b), ptr(ro), ptr(h), st);
+  });
+}
+
+// r_out, dr_out, dh, w, dr, dw, db, ws, eps, stream
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guard([&]() -> PyObject* {
+    Call c(a, n, 10, "layer_norm_backward");
+    const at::Tensor& r = c.need(0, "r_out");
+    const at::Tensor* dro = c.tensor(1, "dr_out");
+    const at::Tensor &dh = c.need(2, "dh"), &w = c.need(3, "w"), &dr = c.need(4, "dr");
+    const at::Tensor *dw = c.tensor(5, "dw"), *db = c.tensor(6, "db"), *ws = c.tensor(7, "ws");
+    const moe_layer_norm_shape s = layer_norm_shape(r, nullptr, w, c.number(8));
+    const ScalarType t = w.scalar_type();
+    want(&r, "r_out", {s.T, s.H}, {t, kF32});
+    want(dro, "dr_out", {s.T, s.H}, {r.scalar_type()});
+    want(&dh, "dh", {s.T, s.H}, {t});
+    want(&w, "w", {s.H}, {t});
+    want(&dr, "dr", {s.T, s.H}, {r.scalar_type()});
+    want(dw, "dw", {s.H}, {kF32});
+    want(db, "db", {s.H}, {kF32});
+    void* st;
+    if (!c.stream(9, &st)) return other_device(c);
+    return run(f_layer_norm_backward, &s, ptr(r), ptr(dro), ptr(dh), ptr(w), ptr(dr),
+               static_cast<float*>(ptr(dw)), static_cast<float*>(ptr(db)), ptr(ws), bytes(ws), st);
+  });
+}
+
+// x, q, scale, stream
+PyObject* quant_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guard([&]() -> PyObject* {
+    Call c(a, n, 4, "quant_rows");
+    const at::Tensor &x = c.need(0, "x"), &q = c.need(1, "q"), &s = c.need(2, "scale");
+    if (x.dim() != 2) refuse("x has shape " + shape_text(x.sizes()) + "; [rows, K] is needed");
+    const int64_t rows = x.size(0), K = x.size(1);
+    want(&x, "x", {rows, K}, {kBf, kHf, kF32});
+    want(&q, "q", {rows, K}, {kI8});
+    want(&s, "scale", {rows}, {kF32});
+    void* st;
+    if (!c.stream(3, &st)) return other_device(c);
+    return run(f_quant_rows, ptr(x), type_code(x.scalar_type()), dim32(rows, "rows"),
+               dim32(K, "K"), static_cast<int8_t*>(ptr(q)), static_cast<float*>(ptr(s)), st);
+  });
+}
+
+// x, x_scale, w, w_scale, bias, residual, y, ws, act, stream
+PyObject* linear_w8a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guard([&]() -> PyObject* {
+    Call c(a, n, 10, "linear_w8a8");
+    const at::Tensor& x = c.need(0, "x");
+    const at::Tensor* xs = c.tensor(1, "x_scale");
+    const at::Tensor &w = c.need(2, "w"), &u = c.need(3, "w_scale");
+    const at::Tensor *bias = c.tensor(4, "bias"), *res = c.tensor(5, "residual");
+    const at::Tensor& y = c.need(6, "y");
+    const at::Tensor* ws = c.tensor(7, "ws");
+    if (x.dim() != 2 || w.dim() != 2)
+      refuse("x has shape " + shape_text(x.sizes()) + ", w " + shape_text(w.sizes()));
+    moe_w8_shape s = {};
+    s.rows = dim32(x.size(0), "rows");
+    s.K = dim32(x.size(1), "K");
+    s.N = dim32(w.size(0), "N");
+    s.act = c.integer(8, "act");
+    s.x_dtype = type_code(x.scalar_type());
+    s.y_dtype = type_code(y.scalar_type());
+    want(&x, "x", {s.rows, s.K}, {kI8, kBf, kHf});
+    want(&w, "w", {s.N, s.K}, {kI8});
+    want(xs, "x_scale", {s.rows}, {kF32});
+    if ((s.x_dtype == MOE_INT8) != (xs != nullptr))
+      refuse("x_scale goes with int8 codes in x, and they with it");
+    want(&u, "w_scale", {s.N}, {kF32});
+    want(bias, "bias", {s.N}, {kF32});
+    want(&y, "y", {s.rows, s.act == MOE_ACT_SWIGLU ? s.N / 2 : s.N}, {kBf, kHf, kF32});
+    want(res, "residual", {y.size(0), y.size(1)}, {y.scalar_type()});
+    void* st;
+    if (!c.stream(9, &st)) return other_device(c);
+    return run(f_linear_w8a8, &s, ptr(x), static_cast<float*>(ptr(xs)), static_cast<int8_t*>(ptr(w)),
+               static_cast<float*>(ptr(u)), static_cast<float*>(ptr(bias)), ptr(res), ptr(y), ptr(ws),
+               bytes(ws), st);
+  });
+}
+
+// logits, x, w13, s13, w2, s2, residual, topk_ids, topk_w, expert_offsets, out, ws, stream
+PyObject* layer_w8a8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guard([&]() -> PyObject* {
+    Call c(a, n, 13, "layer_w8a8");
+    const at::Tensor &L = c.need(0, "logits"), &x = c.need(1, "x"), &w13 = c.need(2, "w13"),
+                     &s13 = c.need(3, "s13"), &w2 = c.need(4, "w2"), &s2 = c.need(5, "s2");
+    const at::Tensor* res = c.tensor(6, "residual");
+    const at::Tensor &ids = c.need(7, "topk_ids"), &w = c.need(8, "topk_w");
+    const at::Tensor* off = c.tensor(9, "expert_offsets");
+    const at::Tensor &out = c.need(10, "out"), &ws = c.need(11, "ws");
+    if (x.dim() != 2 || w13.dim() != 3 || w2.dim() != 3 || ids.dim() != 2)
+      refuse("x has shape " + shape_text(x.sizes()) + ", w13 " + shape_text(w13.sizes()) + ", w2 " +
+             shape_text(w2.sizes()) + ", topk_ids " + shape_text(ids.sizes()));
+    moe_shape s = {};
+    s.T = dim32(x.size(0), "T");
+    s.H = dim32(x.size(1), "H");
+    s.I = dim32(w2.size(2), "I");
+    s.E = dim32(w2.size(0), "E");
+    s.k = dim32(ids.size(1), "k");
+    const int64_t I2 = 2 * static_cast<int64_t>(s.I);
+    want(&L, "logits", {s.T, s.E}, {kF32});
+    want(&x, "x", {s.T, s.H}, {kBf, kHf});
+    want(&w13, "w13", {s.E, I2, s.H}, {kI8});
+    want(&s13, "s13", {s.E, I2}, {kF32});
+    want(&w2, "w2", {s.E, s.H, s.I}, {kI8});
+    want(&s2, "s2", {s.E, s.H}, {kF32});
+    want(&ids, "topk_ids", {s.T, s.k}, {kI32});
+    want(&w, "topk_w", {s.T, s.k}, {kF32});
+    want(off, "expert_offsets", {s.E + int64_t{1}}, {kI32});
+    want(&out, "out", {s.T, s.H}, {kBf, kHf, kF32});
+    want(res, "residual", {s.T, s.H}, {out.scalar_type()});
+    void* st;
+    if (!c.stream(12, &st)) return other_device(c);
+    return run(f_layer_w8a8, &s, static_cast<float*>(ptr(L)), ptr(x), type_code(x.scalar_type()),
+               static_cast<int8_t*>(ptr(w13)), static_cast<float*>(ptr(s13)),
+               static_cast<int8_t*>(ptr(w2)), static_cast<float*>(ptr(s2)), ptr(res),
+               static_cast<int32_t*>(ptr(ids)), static_cast<float*>(ptr(w)),
+               static_cast<int32_t*>(ptr(off)), ptr(out), type_code(out.scalar_type()), ptr(ws),
+               bytes(&ws), st);
+  });
+}
+
+// init(addresses of the entry points in the order of `entry`, get_device, get_stream,
+// has_gpu)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 10) {
-    PyErr_SetString(PyExc_TypeError, "init takes 10 arguments");
+  void** const entry[] = {reinterpret_cast<void**>(&f_grouped_mm),
+                          reinterpret_cast<void**>(&f_grouped_mm_backward),
+                          reinterpret_cast<void**>(&f_linear),
+                          reinterpret_cast<void**>(&f_linear_backward),
+                          reinterpret_cast<void**>(&f_block_norm),
+                          reinterpret_cast<void**>(&f_block_norm_backward),
+                          reinterpret_cast<void**>(&f_combine_backward),
+                          reinterpret_cast<void**>(&f_layer_norm),
+                          reinterpret_cast<void**>(&f_layer_norm_backward),
+                          reinterpret_cast<void**>(&f_quant_rows),
+                          reinterpret_cast<void**>(&f_linear_w8a8),
+                          reinterpret_cast<void**>(&f_layer_w8a8)};
+  constexpr Py_ssize_t kEntries = sizeof(entry) / sizeof(entry[0]);
+  if (n != kEntries + 3) {
+    PyErr_Format(PyExc_TypeError, "init takes %zd arguments", kEntries + 3);
     return nullptr;
   }
-  void* p[7];
-  for (int i = 0; i < 7; ++i) {
-    p[i] = PyLong_AsVoidPtr(a[i]);
+  for (Py_ssize_t i = 0; i < kEntries; ++i) {
+    *entry[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  f_grouped_mm = reinterpret_cast<decltype(f_grouped_mm)>(p[0]);
-  f_grouped_mm_backward = reinterpret_cast<decltype(f_grouped_mm_backward)>(p[1]);
-  f_linear = reinterpret_cast<decltype(f_linear)>(p[2]);
-  f_linear_backward = reinterpret_cast<decltype(f_linear_backward)>(p[3]);
-  f_block_norm = reinterpret_cast<decltype(f_block_norm)>(p[4]);
-  f_block_norm_backward = reinterpret_cast<decltype(f_block_norm_backward)>(p[5]);
-  f_combine_backward = reinterpret_cast<decltype(f_combine_backward)>(p[6]);
-  Py_XINCREF(a[7]);
-  Py_XINCREF(a[8]);
-  g_get_device = a[7];
-  g_get_stream = a[8];
-  g_has_gpu = PyObject_IsTrue(a[9]) == 1;
+  a += kEntries;
+  Py_XINCREF(a[0]);
+  Py_XINCREF(a[1]);
+  g_get_device = a[0];
+  g_get_stream = a[1];
+  g_has_gpu = PyObject_IsTrue(a[2]) == 1;
   Py_RETURN_NONE;
 }
 
@@ -489,6 +659,11 @@ PyMethodDef methods[] = {METHOD(init),
                          METHOD(block_norm),
                          METHOD(block_norm_backward),
                          METHOD(combine_backward),
+                         METHOD(layer_norm),
+                         METHOD(layer_norm_backward),
+                         METHOD(quant_rows),
+                         METHOD(linear_w8a8),
+                         METHOD(layer_w8a8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

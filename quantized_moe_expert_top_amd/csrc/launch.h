@@ -48,6 +48,15 @@ hipError_t launch_w8a8_ffn(int T, int H, int I, int E, int k, const uint16_t* x,
                            const int* active, const int* n_active, float* y,
                            const W8A8Debug& dbg, void* ws, hipStream_t s);
 
+// Its two products on rows that are codes already: h float32 [T k, I] of xq [T, H], y of
+// hq [T k, I].
+hipError_t launch_w8a8_gateup(int T, int H, int I, int E, int k, const int8_t* xq, const float* xs,
+                              const int8_t* w13, const float* s13, const int* offsets,
+                              const int* sorted_slot, float* h, int32_t* dbg_acc, hipStream_t s);
+hipError_t launch_w8a8_down(int T, int H, int I, int E, int k, const int8_t* hq, const float* hs,
+                            const int8_t* w2, const float* s2, const int* offsets,
+                            const int* sorted_slot, float* y, int32_t* dbg_acc, hipStream_t s);
+
 struct W4A8Debug {
   int8_t* xq;
   float* xs;

@@ -82,6 +82,26 @@ int norm_backward_blocks(int T, int H);
 hipError_t launch_block_norm_backward(const NormArgs& a, bool fp16, float* dw_pre, float* dw_post,
                                       float* dgate_channel, hipStream_t s);
 
+struct LayerNormArgs {
+  const void* r;        // forward: r; backward: r_out
+  const void* y;
+  const void* w;
+  const void* b;
+  void* r_out;
+  void* h;
+  const void* dr_out;
+  const void* dh;
+  void* dr;
+  float* part;          // [blocks][2][H]: sums over tokens
+  int T, H;
+  int r_f32, y_f32;
+  float eps;
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, bool fp16, hipStream_t s);
+int layer_norm_backward_blocks(int T, int H);
+hipError_t launch_layer_norm_backward(const LayerNormArgs& a, bool fp16, float* dw, float* db,
+                                      hipStream_t s);
+
 hipError_t launch_combine_backward(const float* dout, const float* y, const int* slot_pos,
                                    const int* ids, const float* w, int T, int H, int E, int k,
                                    void* dy, int dy_type, float* dw, float* dlogits,

@@ -1,0 +1,47 @@
+// Host-side launchers of the int8 operators (moe_int8.h). Arguments have been
+// validated by int8_api.cpp; each returns the launch status.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+// Types: 0 bf16, 1 fp16, 2 float32.
+hipError_t launch_quant_rows(const void* x, int x_type, int rows, int K, int8_t* q, float* scale,
+                             hipStream_t s);
+
+struct LinearI8 {
+  const int8_t* q;        // [rows, K]
+  const float* q_scale;   // [rows]
+  const int8_t* w;        // [N, K]
+  const float* w_scale;   // [N]
+  const float* bias;      // [N] or NULL
+  const void* residual;   // like y, or NULL
+  void* y;
+  int y_type;
+  int rows, K, N, act;
+};
+// check: nothing is launched; hipErrorInvalidConfiguration where the launch would hold
+// 2^32 threads or more.
+hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check);
+
+struct LayerI8 {
+  const float* logits;
+  const void* x;
+  const int8_t* w13;
+  const float* s13;
+  const int8_t* w2;
+  const float* s2;
+  const void* residual;   // like out, or NULL
+  int* ids;
+  float* w;
+  int* offsets;           // [E + 1] or NULL
+  void* out;
+  int x_type, out_type;   // x: 0 or 1
+  int T, H, I, E, k;
+};
+size_t layer_w8a8_workspace_bytes(int T, int H, int I, int E, int k);
+hipError_t launch_layer_w8a8(const LayerI8& l, void* ws, hipStream_t s);
+
+}  // namespace moe

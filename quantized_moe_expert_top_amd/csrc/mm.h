@@ -40,10 +40,30 @@ typedef i32x4_t frag_t;   // 8 values of one operand
 
 struct bf16_tag {};
 struct fp16_tag {};
+// int8 operands (NT only), 16-bit results of type O. A 16-byte fragment holds 16 k
+// values instead of 8 and one MFMA takes 32 instead of 16, so everything that counts
+// bytes holds as it stands: kdim is the contraction length in units of two codes. The
+// accumulators are int32 in the registers of the float32 ones, exact to the epilogue,
+// which rounds each to float32 once and multiplies by the scales of its row and column.
+template <class O>
+struct i8_tag {};
+template <class T>
+struct mm_type {
+  typedef T out;   // the 16-bit type of results
+  static constexpr bool kI8 = false;
+};
+template <class O>
+struct mm_type<i8_tag<O>> {
+  typedef O out;
+  static constexpr bool kI8 = true;
+};
 
 template <class T>
 __device__ __forceinline__ f32x16_t mfma16(frag_t a, frag_t b, f32x16_t c) {
-  if constexpr (__is_same(T, bf16_tag))
+  if constexpr (mm_type<T>::kI8)
+    return __builtin_bit_cast(f32x16_t, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                                            a, b, __builtin_bit_cast(i32x16_t, c), 0, 0, 0));
+  else if constexpr (__is_same(T, bf16_tag))
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   else
@@ -182,6 +202,21 @@ __device__ __forceinline__ void mm_area8(const float* p, float (&v)[8]) {
     v[4 + t] = b[t];
   }
 }
+// An accumulator as float32
+template <class T>
+__device__ __forceinline__ float mm_sum(float v) {
+  if constexpr (mm_type<T>::kI8) return static_cast<float>(__float_as_int(v));
+  else return v;
+}
+// v = v row col + bias, for 8 columns
+__device__ __forceinline__ void mm_scale8(float row, const float* col, const float* bias,
+                                          float (&v)[8]) {
+  float c[8], b[8];
+  mm_area8(col, c);
+  mm_area8(bias, b);
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = __builtin_fmaf(v[t] * row, c[t], b[t]);
+}
 template <class T>
 __device__ __forceinline__ void mm_add8(const uint4& w, float (&v)[8]) {
   const uint32_t d[4] = {w.x, w.y, w.z, w.w};
@@ -221,6 +256,8 @@ struct MMArgs {
   const int* slot;       // gather of the rows of x (NT: A, TN: B), or NULL
   const void* bias;      // [n], or NULL (NT)
   const void* residual;  // like C, or NULL (NT)
+  const float* a_scale;  // [rows], int8 operands: their scales, and float32 bias
+  const float* b_scale;  // [n]
   void* z;               // [rows][N] of T, or NULL (NT)
   void* C;
   int rows;              // grouped rows
@@ -415,7 +452,7 @@ __device__ __forceinline__ bool mm_find_tile(const int* __restrict__ offsets, in
 }
 
 // One tile: block `bid` of a grid of its mode's tiles.
-template <class T, int MODE, class G>
+template <class TT, int MODE, class G>
 __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
                                         const uint8_t* __restrict__ Bb, const MMArgs& a,
                                         uint32_t bid) {
@@ -424,6 +461,9 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
   constexpr int RW = BM / G::WM, CW = BN / G::WN;   // tile rows / columns per wave
   constexpr bool kAK = MODE != kModeTN;             // A is K-major
   constexpr bool kBK = MODE == kModeNT;             // B is K-major
+  constexpr bool kI8 = mm_type<TT>::kI8;
+  typedef typename mm_type<TT>::out T;
+  static_assert(!kI8 || MODE == kModeNT, "int8 operands");
   extern __shared__ __attribute__((aligned(16))) uint8_t mm_lds[];   // G::kLds
   __shared__ int row_src[MODE == kModeTN ? kMMSegRows : BM];
   __shared__ int sm_tile[NTHR / kWave + 4];
@@ -669,7 +709,7 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
 #pragma unroll
     for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma16<T>(fb[j], fa[i], acc[i][j]);
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma16<TT>(fb[j], fa[i], acc[i][j]);
   };
   constexpr std::integral_constant<int, 0> c0{};
   constexpr std::integral_constant<int, MI / 2> c1{};
@@ -738,7 +778,7 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
     uint4 bias, bias_up, res, res_hi;   // bias_up: SwiGLU; res_hi: float32
   };
   auto load_added = [&](int row, int col, Added& v) {
-    if (a.bias) {
+    if (!kI8 && a.bias) {
       v.bias = ld16(static_cast<const uint16_t*>(a.bias) + col);
       if (swiglu) v.bias_up = ld16(static_cast<const uint16_t*>(a.bias) + half_n + col);
     }
@@ -765,6 +805,21 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
     load_piece(0, lane + kWave, ahead[1]);
   }
 
+  // int8: the tile's scales and biases, one of each to a thread, requested here and
+  // laid into LDS after the products
+  static_assert(!kI8 || (BM <= NTHR && BN <= NTHR), "a thread holds one scale");
+  __shared__ __attribute__((aligned(16))) float i8_row[kI8 ? BM : 4], i8_col[kI8 ? BN : 4],
+      i8_bias[kI8 ? BN : 4];
+  float s_row = 0.0f, s_col = 0.0f, s_bias = 0.0f;
+  if constexpr (kI8) {
+    if (tid < mrows) s_row = a.a_scale[m0 + tid];
+    const int src = tid < BN ? b_row(tid) : -1;
+    if (src >= 0) {
+      s_col = a.b_scale[src];
+      if (a.bias) s_bias = static_cast<const float*>(a.bias)[src];
+    }
+  }
+
   constexpr int kSegSteps = kMMSegRows / BK;
   const int seg_len = MODE == kModeTN && gather ? kSegSteps : steps;
   for (int seg0 = 0; seg0 < steps; seg0 += seg_len) {
@@ -789,6 +844,13 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
   // float32 area of LDS that is the wave's own, from where 8 columns of a row go
   // to a lane: whole row pieces are read and written (bias, residual, z, C), and
   // the activation's code stands once instead of once per accumulator.
+  if constexpr (kI8) {
+    if (tid < BM) i8_row[tid] = s_row;
+    if (tid < BN) {
+      i8_col[tid] = s_col;
+      i8_bias[tid] = s_bias;
+    }
+  }
   __syncthreads();   // the stages are read
   if (!live) return;
   constexpr int kRowF = CW + 4;   // floats per row of the area; + 4: banks
@@ -811,8 +873,8 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<f32x4_t*>(area + l32 * kRowF + j * 32 + q * 8 + hf * 4) =
-                f32x4_t{acc[x][j][q * 4], acc[x][j][q * 4 + 1], acc[x][j][q * 4 + 2],
-                        acc[x][j][q * 4 + 3]};
+                f32x4_t{mm_sum<TT>(acc[x][j][q * 4]), mm_sum<TT>(acc[x][j][q * 4 + 1]),
+                        mm_sum<TT>(acc[x][j][q * 4 + 2]), mm_sum<TT>(acc[x][j][q * 4 + 3])};
       }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -825,7 +887,8 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
       float v[8];
       mm_area8(area + r * kRowF + c, v);
       if constexpr (MODE == kModeNT) {
-        if (ADDED && a.bias) mm_add8<T>(add.bias, v);
+        if constexpr (kI8) mm_scale8(i8_row[row], i8_col + wn * CW + c, i8_bias + wn * CW + c, v);
+        else if (ADDED && a.bias) mm_add8<T>(add.bias, v);
         const uint32_t zoff = (static_cast<uint32_t>(row) * a.ndim + col) * 2;
         if (a.z) {
           mm_put16(mm_pack8<T>(v), z_rs, zoff, stream);
@@ -833,7 +896,9 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
         if (swiglu) {
           float u[8];
           mm_area8(area + r * kRowF + CW / 2 + c, u);
-          if (ADDED && a.bias) mm_add8<T>(add.bias_up, u);
+          if constexpr (kI8)
+            mm_scale8(i8_row[row], i8_col + wn * CW + CW / 2 + c, i8_bias + wn * CW + CW / 2 + c, u);
+          else if (ADDED && a.bias) mm_add8<T>(add.bias_up, u);
           if (a.z) mm_put16(mm_pack8<T>(u), z_rs, zoff + half_n * 2, stream);
           auto gated = [&](auto exact) {
 #pragma unroll
@@ -875,7 +940,7 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
       static_assert(CW == 32, "two pieces per lane");
       piece(lane, ahead[0], std::true_type{});
       if (!swiglu) piece(lane + kWave, ahead[1], std::true_type{});
-    } else if (MODE == kModeNT && (a.bias || a.residual)) {
+    } else if (MODE == kModeNT && ((!kI8 && a.bias) || a.residual)) {
       for (int it = lane; it < 32 * per_row; it += kWave) {
         const bool last = it + kWave >= 32 * per_row;
         ahead[1] = ahead[0];

@@ -7,7 +7,8 @@
 // from memory straight into the registers of v_mfma_f32_16x16x32 (each W value is
 // used once: staging it would only add latency), U steps ahead. The waves'
 // partial tiles are added in LDS in wave order, so the result does not depend
-// on timing.
+// on timing. int8 operands (i8_tag): the same with v_mfma_i32_16x16x64, k counted in
+// units of two codes.
 #pragma once
 #include "mm_launch.h"
 
@@ -15,7 +16,10 @@ namespace moe {
 
 template <class T>
 __device__ __forceinline__ f32x4_t mfma16x16(frag_t a, frag_t b, f32x4_t c) {
-  if constexpr (__is_same(T, bf16_tag))
+  if constexpr (mm_type<T>::kI8)   // 64 k of int8
+    return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                           a, b, __builtin_bit_cast(i32x4_t, c), 0, 0, 0));
+  else if constexpr (__is_same(T, bf16_tag))
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   else
@@ -23,11 +27,30 @@ __device__ __forceinline__ f32x4_t mfma16x16(frag_t a, frag_t b, f32x4_t c) {
                                                   __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-template <class T, int MT, int WAVES, int U>
+// Sum of the waves' partial results of one output, as float32 (int8: the integers are
+// added first, exactly)
+template <class T, int WAVES, int BM>
+__device__ __forceinline__ float mm_few_sum(const float (&part)[WAVES][BM][16], int r, int c) {
+  if constexpr (mm_type<T>::kI8) {
+    int v = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += __float_as_int(part[w][r][c]);
+    return static_cast<float>(v);
+  } else {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += part[w][r][c];
+    return v;
+  }
+}
+
+template <class TT, int MT, int WAVES, int U>
 __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __restrict__ Ab,
                                                             const uint8_t* __restrict__ Bb,
                                                             const MMArgs a) {
   constexpr int BM = 16 * MT, NTHR = WAVES * kWave;
+  constexpr bool kI8 = mm_type<TT>::kI8;
+  typedef typename mm_type<TT>::out T;
   __shared__ __attribute__((aligned(16))) float part[WAVES][BM][16];
   __shared__ int sm_tile[NTHR / kWave + 4];
   MMTile t;
@@ -89,11 +112,19 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
   struct Added {
     uint16_t bias, bias_up, res;
     float res_f;
+    float s_row, s_col, s_up, bias_f, bias_up_f;   // int8
   };
   auto load_added = [&](int it, Added& v) {
     const int r = it / cols, col = n0 + it - r * cols;
     if (r >= mrows || col >= out_w) return;
-    if (a.bias) {
+    if constexpr (kI8) {
+      const float* b = static_cast<const float*>(a.bias);
+      v.s_row = a.a_scale[static_cast<size_t>(t.p0) + r];
+      v.s_col = a.b_scale[col];
+      v.s_up = swiglu ? a.b_scale[half_n + col] : 0.0f;
+      v.bias_f = b ? b[col] : 0.0f;
+      v.bias_up_f = b && swiglu ? b[half_n + col] : 0.0f;
+    } else if (a.bias) {
       v.bias = static_cast<const uint16_t*>(a.bias)[col];
       if (swiglu) v.bias_up = static_cast<const uint16_t*>(a.bias)[half_n + col];
     }
@@ -111,7 +142,7 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = mfma16x16<T>(wr[d][h], xr[d][h][i], acc[i]);
+        for (int i = 0; i < MT; ++i) acc[i] = mfma16x16<TT>(wr[d][h], xr[d][h][i], acc[i]);
       load(s + (d + U) * WAVES, wr[d], xr[d]);
     }
   }
@@ -126,20 +157,21 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
     if (col >= out_w) continue;
     if (it != tid) load_added(it, add);
     const size_t p = static_cast<size_t>(t.p0) + r;
-    float v = 0.0f, g = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += part[w][r][c];
+    float v = mm_few_sum<TT>(part, r, c), g = 0.0f;
     uint16_t* z = static_cast<uint16_t*>(a.z);
     float lo, hi;
-    if (a.bias) {
+    if constexpr (kI8) {
+      v = __builtin_fmaf(v * add.s_row, add.s_col, add.bias_f);
+    } else if (a.bias) {
       unpack2<T>(add.bias, lo, hi);
       v += lo;
     }
     if (z) z[p * a.ndim + col] = static_cast<uint16_t>(pack2<T>(v, 0.0f));
     if (swiglu) {
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) g += part[w][r][8 + c];
-      if (a.bias) {
+      g = mm_few_sum<TT>(part, r, 8 + c);
+      if constexpr (kI8) {
+        g = __builtin_fmaf(g * add.s_row, add.s_up, add.bias_up_f);
+      } else if (a.bias) {
         unpack2<T>(add.bias_up, lo, hi);
         g += lo;
       }

@@ -558,15 +558,26 @@ hipError_t launch_w8a8_ffn(int T, int H, int I, int E, int k, const uint16_t* x,
       x, T, H, w.xq, w.xs, dbg.xq, dbg.xs);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  err = launch_w8a8_gemm<0, W8Tile>(w.xq, w.xs, w13, s13, offsets, sorted_slot, H, 2 * I, E, k, T,
-                                   w.h, nullptr, dbg.acc13, s);
+  err = launch_w8a8_gateup(T, H, I, E, k, w.xq, w.xs, w13, s13, offsets, sorted_slot, w.h, dbg.acc13, s);
   if (err != hipSuccess) return err;
   h_quant_kernel<<<(R + rows_per_block - 1) / rows_per_block, kThreads, 0, s>>>(
       w.h, R, I, w.hq, w.hs, dbg.hq, dbg.hs);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  return launch_w8a8_gemm<1, W8Tile>(w.hq, w.hs, w2, s2, offsets, sorted_slot, I, H, E, k, T,
-                                    nullptr, y, dbg.acc2, s);
+  return launch_w8a8_down(T, H, I, E, k, w.hq, w.hs, w2, s2, offsets, sorted_slot, y, dbg.acc2, s);
+}
+
+hipError_t launch_w8a8_gateup(int T, int H, int I, int E, int k, const int8_t* xq, const float* xs,
+                              const int8_t* w13, const float* s13, const int* offsets,
+                              const int* sorted_slot, float* h, int32_t* dbg_acc, hipStream_t s) {
+  return launch_w8a8_gemm<0, W8Tile>(xq, xs, w13, s13, offsets, sorted_slot, H, 2 * I, E, k, T, h,
+                                     nullptr, dbg_acc, s);
+}
+hipError_t launch_w8a8_down(int T, int H, int I, int E, int k, const int8_t* hq, const float* hs,
+                            const int8_t* w2, const float* s2, const int* offsets,
+                            const int* sorted_slot, float* y, int32_t* dbg_acc, hipStream_t s) {
+  return launch_w8a8_gemm<1, W8Tile>(hq, hs, w2, s2, offsets, sorted_slot, I, H, E, k, T, nullptr, y,
+                                     dbg_acc, s);
 }
 
 }  // namespace moe
