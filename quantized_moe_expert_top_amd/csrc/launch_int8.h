@@ -26,6 +26,21 @@ struct LinearI8 {
 // 2^32 threads or more.
 hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check);
 
+// out[p] = (q[src(p)] . W_e^T) scaled, float32, for the rows p of each expert e; src(p) =
+// slot[p] / topk, or p where slot is NULL. swiglu: N is 2 I, out [rows, I].
+struct GroupedI8 {
+  const int8_t* q;        // [q_rows, K]
+  const float* q_scale;   // [q_rows]
+  const int8_t* w;        // [E, N, K]
+  const float* w_scale;   // [E, N]
+  const int* offsets;     // [E + 1]
+  const int* slot;        // [rows] or NULL
+  float* out;
+  int rows, q_rows, topk, E, K, N;
+  bool swiglu;
+};
+hipError_t launch_grouped_i8(const GroupedI8& g, hipStream_t s);
+
 struct LayerI8 {
   const float* logits;
   const void* x;

@@ -256,8 +256,8 @@ struct MMArgs {
   const int* slot;       // gather of the rows of x (NT: A, TN: B), or NULL
   const void* bias;      // [n], or NULL (NT)
   const void* residual;  // like C, or NULL (NT)
-  const float* a_scale;  // [rows], int8 operands: their scales, and float32 bias
-  const float* b_scale;  // [n]
+  const float* a_scale;  // int8 operands: a scale for each row of x and of W; float32 bias
+  const float* b_scale;
   void* z;               // [rows][N] of T, or NULL (NT)
   void* C;
   int rows;              // grouped rows
@@ -812,10 +812,10 @@ __device__ __forceinline__ void mm_tile(const uint8_t* __restrict__ Ab,
       i8_bias[kI8 ? BN : 4];
   float s_row = 0.0f, s_col = 0.0f, s_bias = 0.0f;
   if constexpr (kI8) {
-    if (tid < mrows) s_row = a.a_scale[m0 + tid];
+    if (tid < mrows) s_row = a.a_scale[gather ? row_src[tid] : m0 + tid];
     const int src = tid < BN ? b_row(tid) : -1;
     if (src >= 0) {
-      s_col = a.b_scale[src];
+      s_col = a.b_scale[static_cast<size_t>(e) * a.ndim + src];
       if (a.bias) s_bias = static_cast<const float*>(a.bias)[src];
     }
   }

@@ -119,9 +119,11 @@ __global__ __launch_bounds__(WAVES * 64) void mm_few_kernel(const uint8_t* __res
     if (r >= mrows || col >= out_w) return;
     if constexpr (kI8) {
       const float* b = static_cast<const float*>(a.bias);
-      v.s_row = a.a_scale[static_cast<size_t>(t.p0) + r];
-      v.s_col = a.b_scale[col];
-      v.s_up = swiglu ? a.b_scale[half_n + col] : 0.0f;
+      const float* u = a.b_scale + static_cast<size_t>(t.e) * a.ndim;
+      const int p = t.p0 + r;
+      v.s_row = a.a_scale[a.slot ? min(max(a.slot[p] / a.topk, 0), a.x_rows - 1) : p];
+      v.s_col = u[col];
+      v.s_up = swiglu ? u[half_n + col] : 0.0f;
       v.bias_f = b ? b[col] : 0.0f;
       v.bias_up_f = b && swiglu ? b[half_n + col] : 0.0f;
     } else if (a.bias) {

@@ -26,6 +26,27 @@ hipError_t launch(const MMArgs& a, int plan, hipStream_t s, bool check) {
 
 }  // namespace
 
+hipError_t launch_grouped_i8(const GroupedI8& g, hipStream_t s) {
+  MMArgs a = {};
+  a.A = g.q;
+  a.B = g.w;
+  a.a_scale = g.q_scale;
+  a.b_scale = g.w_scale;
+  a.offsets = g.offsets;
+  a.slot = g.slot;
+  a.x_rows = g.q_rows;
+  a.topk = g.topk;
+  a.C = g.out;
+  a.rows = g.rows;
+  a.E = g.E;
+  a.splits = 1;
+  a.ndim = g.N;
+  a.kdim = g.K / 2;
+  a.act = g.swiglu ? kActSwiglu : 0;
+  a.c_f32 = 1;
+  return launch<i8_tag<bf16_tag>>(a, mm_forward_plan(g.rows, g.E, g.N, g.K / 2, a.act), s, false);
+}
+
 hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
   MMArgs a = {};
   a.A = l.q;

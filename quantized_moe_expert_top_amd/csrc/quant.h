@@ -11,13 +11,55 @@ namespace moe {
 // NaN above them: no value is dropped, as fmaxf drops NaN.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
+
+// Eight values of a row as they are stored: 16 bytes of T, or 32 of float32.
+template <class T, bool F32>
+struct Vals8 {
+  uint4 lo, hi;   // hi: float32 only
+  __device__ __forceinline__ void load(const void* x, size_t at) {
+    if constexpr (F32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at);
+      lo = p[0];
+      hi = p[1];
+    } else {
+      lo = ld16(static_cast<const uint16_t*>(x) + at);
+    }
+  }
+  // the largest |x| as float32 bits. 16-bit values are compared as they are, two at a time.
+  __device__ __forceinline__ uint32_t amax(uint32_t m) const {
+    if constexpr (F32) {
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_u32(m, abs_bits(v[i]));
-  return m;
-}
+      for (int i = 0; i < 8; ++i) m = max_u32(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      typedef __attribute__((__vector_size__(2 * sizeof(uint16_t)))) uint16_t u16x2_t;
+      auto mx = [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                      __builtin_bit_cast(u16x2_t, b)));
+      };
+      const uint32_t w = mx(mx(lo.x & 0x7FFF7FFFu, lo.y & 0x7FFF7FFFu), mx(lo.z & 0x7FFF7FFFu, lo.w & 0x7FFF7FFFu));
+      float a, b;
+      unpack2<T>(max_u32(w & 0xFFFFu, w >> 16), a, b);
+      return max_u32(m, __float_as_uint(a));
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (F32) {
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+      unpack2<T>(lo.x, v[0], v[1]);
+      unpack2<T>(lo.y, v[2], v[3]);
+      unpack2<T>(lo.z, v[4], v[5]);
+      unpack2<T>(lo.w, v[6], v[7]);
+    }
+  }
+};
+
 struct RowScale {
-  float s, r;   // the scale, and 1 / s (0 where every code is 0, infinite where s is
+  float s, r;   // the scale, and about 1 / s (0 where every code is 0, infinite where s is
                 // subnormal and so far off amax / 127 that a code may pass 127)
 };
 __device__ __forceinline__ RowScale row_scale(uint32_t amax) {
@@ -26,43 +68,38 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax) {
   q.s = finite ? __uint_as_float(amax) / 127.0f : __uint_as_float(0x7FC00000u);
   q.r = !finite || q.s == 0.0f ? 0.0f
         : q.s < 1.17549435e-38f ? __uint_as_float(0x7F800000u)
-                                : 1.0f / q.s;
-  return q;
-}
-// The code of v. v r is within 2^-22 of the float32 quotient v / s, relative (r rounds
-// once, the product once, the quotient once: 1.5 x 2^-23), so within 127 x 2^-22 < 3.1e-5
-// of it: where it is further than that from the middle of two whole numbers, both round
-// to the same one. Otherwise (and where r is infinite, so
-// that v r is no number or infinite) `near` is set and the caller divides. A division takes about ten
-// instructions, this takes three.
-__device__ __forceinline__ float code_near(float v, float r, bool& near) {
-  const float p = v * r, q = rintf(p);
-  near |= !(__builtin_fabsf(p - q) < 0.5f - 3.2e-5f);
+                                : __builtin_amdgcn_rcpf(q.s);
   return q;
 }
 __device__ __forceinline__ float code_exact(float v, float s) {
   return __builtin_fminf(__builtin_fmaxf(rintf(v / s), -127.0f), 127.0f);
 }
-__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
-  const uint32_t x = static_cast<uint32_t>(static_cast<int>(a)) & 0xFFu,
-                 y = static_cast<uint32_t>(static_cast<int>(b)) & 0xFFu,
-                 z = static_cast<uint32_t>(static_cast<int>(c)) & 0xFFu,
-                 w = static_cast<uint32_t>(static_cast<int>(d));
-  return x | (y << 8) | (z << 16) | (w << 24);
-}
+// Codes of eight values of one row. v r is within 2^-22 of the float32 quotient v / s,
+// relative (r is off by 2^-23, the quotient rounds once, 2^-24; the fma does not round
+// v r), so within 127 x 2^-22 < 3.1e-5 of it: where v r is further than that from the
+// middle of two whole numbers, both round to the same one. That number is the low byte of
+// v r + 1.5 x 2^23, whose last place is 1. Otherwise, for about one value in 16000, the
+// eight are divided, at about ten instructions each instead of five.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const RowScale& s) {
-  float q[8];
-  bool near = false;
+  constexpr float kBig = 12582912.0f;
+  uint32_t t[8];
+  float off = 0.0f;   // the furthest from a whole number
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = code_near(v[i], s.r, near);
-  if (s.r == 0.0f) {   // uniform over a row: zeros, or no numbers
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = 0.0f;
-  } else if (near) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = code_exact(v[i], s.s);
+  for (int i = 0; i < 8; ++i) {
+    const float b = __builtin_fmaf(v[i], s.r, kBig);
+    off = __builtin_fmaxf(off, __builtin_fabsf(__builtin_fmaf(v[i], s.r, kBig - b)));
+    t[i] = __float_as_uint(b);
   }
-  return make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+  if (s.r == 0.0f) return make_uint2(0, 0);   // uniform over a row: zeros, or no numbers
+  if (!(off < 0.5f - 3.2e-5f) || __builtin_isinf(s.r)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = static_cast<uint32_t>(static_cast<int>(code_exact(v[i], s.s)));
+  }
+  auto pack = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {   // their low bytes
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u),
+                                 0x05040100u);
+  };
+  return make_uint2(pack(t[0], t[1], t[2], t[3]), pack(t[4], t[5], t[6], t[7]));
 }
 
 }  // namespace moe

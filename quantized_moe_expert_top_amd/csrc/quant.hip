@@ -1,7 +1,6 @@
 // Token rows to int8 codes with a scale per row (moe_quant_rows), bound by the bytes of
 // the rows: each is read once and stays in registers between its maximum and its codes.
 #include "launch_int8.h"
-#include "norm_rows.h"
 #include "quant.h"
 
 namespace moe {
@@ -19,13 +18,12 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void quant_rows_kernel(
   if (t >= rows) return;   // whole waves; with WPR > 1, whole blocks
   const int C = K / 8;
   const size_t row = static_cast<size_t>(t) * K;
-  float v[NC][8];
+  Vals8<T, F32> v[NC];
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
-    row_load8<T>(x, row + min(rt + i * kRowThreads, C - 1) * 8, F32, v[i]);   // past the row: its last
+  for (int i = 0; i < NC; ++i) v[i].load(x, row + min(rt + i * kRowThreads, C - 1) * 8);   // past the row: its last
 #pragma unroll
-  for (int i = 0; i < NC; ++i) m = amax8(v[i], m);
+  for (int i = 0; i < NC; ++i) m = v[i].amax(m);
   m = wave_max_u32(m);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x >> 6] = m;
@@ -37,7 +35,10 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void quant_rows_kernel(
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = rt + i * kRowThreads;
-    if (c < C) *reinterpret_cast<uint2*>(q + row + c * 8) = codes8(v[i], s);
+    if (c >= C) continue;
+    float f[8];
+    v[i].values(f);
+    *reinterpret_cast<uint2*>(q + row + c * 8) = codes8(f, s);
   }
   if (rt == 0) scale[t] = s.s;
 }
