@@ -141,6 +141,8 @@ moe_status moe_linear_w8a8(const moe_w8_shape* s, const void* x, const float* x_
   if (moe::launch_linear_w8a8(l, stm, true) != hipSuccess)
     return fail(MOE_ESHAPE, "a launch of these sizes would hold 2^32 threads or more");
   if ((st = check_device()) != MOE_OK) return st;
+  if (!codes && moe::linear_w8a8_makes_codes(l))
+    return launched(moe::launch_linear_w8a8_values(l, x, s->x_dtype, stm), "moe_linear_w8a8 launch");
   if (!codes) {
     st = launched(moe::launch_quant_rows(x, s->x_dtype, s->rows, s->K, made, made_scale, stm),
                   "moe_linear_w8a8 codes launch");

@@ -25,6 +25,10 @@ struct LinearI8 {
 // check: nothing is launched; hipErrorInvalidConfiguration where the launch would hold
 // 2^32 threads or more.
 hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check);
+// Few rows of values (x_type 0 or 1): their codes are made in the product's launch (q and
+// q_scale are not read).
+bool linear_w8a8_makes_codes(const LinearI8& l);
+hipError_t launch_linear_w8a8_values(const LinearI8& l, const void* x, int x_type, hipStream_t s);
 
 // out[p] = (q[src(p)] . W_e^T) scaled, float32, for the rows p of each expert e; src(p) =
 // slot[p] / topk, or p where slot is NULL. swiglu: N is 2 I, out [rows, I].

@@ -1,25 +1,14 @@
 // The W8A8 layer for a few tokens (moe_layer_w8a8), bound by the bytes of the picked
 // experts' weights: two kernels, gate/up and down with the combine.
-//
-// One block per CU holds the codes of all rows in LDS; each of its waves streams units of
-// 16 weight rows through a ring of its own in LDS, 128 bytes of k of every row a step, D
-// steps ahead over the ends of units: a wave load takes 8 rows x 128 bytes, whole cache
-// lines (operands loaded straight into registers take 16 rows x 64 bytes: 4.0 TB/s where
-// this reaches more), and nothing waits for other waves. v_mfma_i32_16x16x64 multiplies
-// the 16 rows with up to 16 rows of codes; int32 sums are exact.
 #pragma once
 #include "../../include/moe.h"
+#include "few.h"
 #include "launch_int8.h"
 #include "norm_rows.h"
-#include "quant.h"
 
 namespace moe {
 
-constexpr int kFewTokens = 16;    // an expert gets a token at most once: one MFMA operand
-constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
-constexpr int kFewBlocks = 256;   // one per CU
 constexpr int kFewMaxR = kFewTokens * MOE_MAX_TOPK;
-constexpr int kFewStep = 128;     // bytes of k of each row a step
 
 // What the gate/up kernel found about the picks, for the down kernel: few_table's list.
 struct FewRecord {
@@ -68,78 +57,6 @@ struct FewArgs {
   void* out;
   int T, H, I, E, k;
 };
-
-// A barrier for what is written to LDS by instructions; __syncthreads would wait for the
-// rings' loads too.
-__device__ __forceinline__ void few_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-// Rows of values [rows, K] to codes in LDS (`stride` bytes a row) and scales by a whole
-// block, in two phases: get() requests this thread's chunks of 8 values and amax() adds to
-// the rows' maxima in LDS; after a barrier put() writes the codes. Every chunk stays in
-// registers, so rows * K is at most kFewValues.
-constexpr int kFewChunks = 4, kFewValues = kFewChunks * 8 * kFewThreads;
-template <class T, bool F32>
-struct FewRows {
-  Vals8<T, F32> v[kFewChunks];
-  uint32_t inv;   // division by the chunks of a row, exact below 2^16
-  __device__ __forceinline__ int row_of(int c) const { return __umulhi(c, inv); }
-  __device__ __forceinline__ void get(const void* x, int rows, int K) {
-    const int C = K / 8, total = rows * C;
-    inv = 0xFFFFFFFFu / C + 1;
-#pragma unroll
-    for (int i = 0; i < kFewChunks; ++i)
-      if (i * kFewThreads < total)   // uniform
-        v[i].load(x, static_cast<size_t>(min(static_cast<int>(threadIdx.x) + i * kFewThreads, total - 1)) * 8);
-  }
-  __device__ __forceinline__ void amax(int rows, int K, uint32_t* m) {
-    const int total = rows * (K / 8);
-#pragma unroll
-    for (int i = 0; i < kFewChunks; ++i) {
-      if (i * kFewThreads >= total) break;
-      const int c = threadIdx.x + i * kFewThreads, r = row_of(min(c, total - 1));
-      const uint32_t a = v[i].amax(0);   // past the end: the last chunk again
-      const int r0 = __builtin_amdgcn_readfirstlane(r);
-      if (__ballot(r != r0) == 0) {
-        const uint32_t w = wave_max_u32(a);
-        if ((threadIdx.x & (kWave - 1)) == 0) atomicMax(&m[r0], w);
-      } else {
-        atomicMax(&m[r], a);
-      }
-    }
-  }
-  __device__ __forceinline__ void put(int rows, int K, const uint32_t* m, uint8_t* to, int stride, float* scale) {
-    const int C = K / 8, total = rows * C;
-#pragma unroll
-    for (int i = 0; i < kFewChunks; ++i) {
-      const int c = threadIdx.x + i * kFewThreads;
-      if (i * kFewThreads >= total) break;
-      if (c >= total) continue;
-      const int r = row_of(c);
-      float f[8];
-      v[i].values(f);
-      *reinterpret_cast<uint2*>(to + r * stride + (c - r * C) * 8) = codes8(f, row_scale(m[r]));
-    }
-    if (static_cast<int>(threadIdx.x) < rows) scale[threadIdx.x] = row_scale(m[threadIdx.x]).s;
-  }
-};
-// The same where the codes are there already: copied.
-__device__ __forceinline__ void few_copy(const int8_t* q, const float* q_scale, int rows, int K, uint8_t* to, int stride,
-                                         float* scale) {
-  const int C = K / 16, total = rows * C;
-  const uint32_t inv = 0xFFFFFFFFu / C + (C > 1);   // C 1: every chunk a row
-  for (int c0 = threadIdx.x; c0 < total; c0 += 4 * kFewThreads) {
-    uint4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ld16(q + static_cast<size_t>(min(c0 + i * kFewThreads, total - 1)) * 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + i * kFewThreads;
-      if (c >= total) break;
-      const int r = C > 1 ? __umulhi(c, inv) : c;
-      *reinterpret_cast<uint4*>(to + r * stride + (c - r * C) * 16) = v[i];
-    }
-  }
-  if (static_cast<int>(threadIdx.x) < rows) scale[threadIdx.x] = q_scale[threadIdx.x];
-}
 
 __device__ __forceinline__ void few_wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -255,27 +172,32 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
   const int l16 = lane & 15, kg = lane >> 4;
   const int R = a.T * a.k;
   const int K = KIND == 0 ? a.H : a.I, rows = KIND == 0 ? a.T : R, stride = K + 16;
-  uint8_t* ring = few_lds + wv * (D * 2048);
-  uint8_t* codes = few_lds + kFewWaves * D * 2048;
+  uint8_t* ring = few_lds + wv * (D * kFewSlot);
+  uint8_t* codes = few_lds + kFewWaves * D * kFewSlot;
   float* s_y = reinterpret_cast<float*>(codes + static_cast<size_t>(rows) * stride);   // KIND 1
 
+  // rows first: loads return in order, so that these are not waited for behind the ring's
   FewRows<T, KIND == 1> made;
+  FewCodes copied;
   if constexpr (!CODES) {
     made.get(KIND == 0 ? a.x : a.h, rows, K);
     if (tid < rows) s_amax[tid] = 0;
+  } else if (KIND == 1) {
+    copied.get(a.hq, a.hs, rows, K);
   }
   int n_act;
   if constexpr (KIND == 0) {
     if constexpr (CODES) {
       if (tid < R) s_ids[tid] = a.ids[tid];
-      few_copy(a.xq, a.xs, rows, K, codes, stride, s_scale);
+      copied.get(a.xq, a.xs, rows, K);
+      copied.put(a.xq, rows, K, codes, stride, s_scale);
     } else {
       few_barrier();   // s_amax is cleared
       if (wv < a.T)
         wave_topk<S>(a.logits + static_cast<size_t>(wv) * a.E, a.E, a.k, s_ids + wv * a.k, s_w + wv * a.k);
       made.amax(rows, K, s_amax);
     }
-    __syncthreads();
+    few_barrier();
     n_act = few_table(s_ids, R, reinterpret_cast<int*>(few_lds), s_act, s_beg, s_sorted);
     if (blockIdx.x == 0) {
       if (!CODES && tid < R) {
@@ -289,11 +211,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
     n_act = a.record->n_act;
     if (tid < R) s_w[tid] = a.w[tid];
     a.record->get(R, s_act, s_beg, s_sorted);
-    if constexpr (CODES) few_copy(a.hq, a.hs, rows, K, codes, stride, s_scale);
-    __syncthreads();
-    // the values have come by now; asked for behind the ring's loads, they would be waited
-    // for with those
-    if constexpr (!CODES) made.amax(rows, K, s_amax);
+    few_barrier();
   }
   n_act = __builtin_amdgcn_readfirstlane(n_act);
 
@@ -327,12 +245,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
     return u;
   };
 
-  // ring slot: lane fills 16 bytes: row lane / 8 of the load's 8, chunk lane % 8, which
-  // holds chunk (lane % 8) ^ (row % 8) of the step, so that the operand reads (16 rows at
-  // one chunk) fall in distinct banks
   const int N = KIND == 0 ? 2 * a.I : a.H;
   const int8_t* W = KIND == 0 ? a.w13 : a.w2;
-  const int lrow = lane >> 3, chunk = (lane & 7) ^ lrow;
+  const int lrow = lane >> 3, chunk = few_chunk(lane);
   // issue cursor
   int iu = 0, is = 0;
   uint32_t off0 = 0, off1 = 0;
@@ -347,22 +262,17 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
       // ring rows 4 q + {0, 1} are gate rows 2 q + {0, 1}, 4 q + {2, 3} the matching up
       // rows, so that a lane ends with both of an output
       const int r0 = u.tile * 8 + (lrow >> 2) * 2 + (lrow & 1) + (lrow & 2 ? a.I : 0);
-      off0 = static_cast<uint32_t>(r0) * K + chunk * 16;
+      off0 = __umul24(r0, K) + chunk * 16;
       off1 = off0 + 4u * K;
     } else {
       const int e1 = u.a1 < 0 ? -1 : __builtin_amdgcn_readfirstlane(s_act[u.a1]);
       rs1 = buffer_rsrc(W + (e1 < 0 ? 0 : e1) * each, e1 < 0 ? 0u : static_cast<uint32_t>(each));
-      off0 = off1 = static_cast<uint32_t>(u.tile * 8 + lrow) * K + chunk * 16;
+      off0 = off1 = __umul24(u.tile * 8 + lrow, K) + chunk * 16;
     }
   };
-  // the loads of one step: always two, so that they can be counted; past the last unit and
-  // past k they read nothing
   auto issue = [&](int slot) {
-    uint8_t* to = ring + slot * 2048;
     const int k0 = is * kFewStep;
-    const bool in = iu < count && k0 + chunk * 16 < K;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs0, (lds_void_t*)to, 16, in ? off0 + k0 : kMMPastEnd, 0, 0, 2);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs1, (lds_void_t*)(to + 1024), 16, in ? off1 + k0 : kMMPastEnd, 0, 0, 2);
+    few_issue(ring + slot * kFewSlot, rs0, off0 + k0, rs1, off1 + k0, iu < count && k0 + chunk * 16 < K);
     if (++is == steps) {
       is = 0;
       if (++iu < count) enter(iu);
@@ -371,18 +281,21 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
   // not the whole ring before the codes are made: loads waiting to be issued would hold that
   // up (layers of 1 to 8 tokens 1 to 2% slower with all of it or half of it)
   constexpr int kFirst = CODES ? D : D / 4 * 3;
-  if (total > 0) {
-    enter(0);
+  // Issued by every wave, whether it has units or not: the compiler counts them.
+  if (total > 0) enter(0);
 #pragma unroll
-    for (int d = 0; d < kFirst; ++d) issue(d);
-  }
+  for (int d = 0; d < kFirst; ++d) issue(d);
   if constexpr (!CODES) {
-    few_barrier();
-    made.put(rows, K, s_amax, codes, stride, s_scale);
-    if (total > 0) {
-#pragma unroll
-      for (int d = kFirst; d < D; ++d) issue(d);
+    if (KIND == 1) {
+      made.amax(rows, K, s_amax);
+      few_barrier();
     }
+    made.put(rows, K, s_amax, codes, stride, s_scale);
+#pragma unroll
+    for (int d = kFirst; d < D; ++d) issue(d);
+    few_barrier();
+  } else if (KIND == 1) {
+    copied.put(a.hq, rows, K, codes, stride, s_scale);
     few_barrier();
   }
 
@@ -442,22 +355,20 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
         float* to = s_y + static_cast<size_t>(u.tile / kFewBlocks) * R * 8 + (kg & 1) * 4;
         auto put = [&](const i32x4_t& acc, int slot) {
           const float hs = s_scale[slot];
-          *reinterpret_cast<f32x4_t*>(to + slot * 8) =
-              f32x4_t{static_cast<float>(acc[0]) * hs * s[0], static_cast<float>(acc[1]) * hs * s[1],
-                      static_cast<float>(acc[2]) * hs * s[2], static_cast<float>(acc[3]) * hs * s[3]};
+          const f32x4_t v = {static_cast<float>(acc[0]) * hs * s[0], static_cast<float>(acc[1]) * hs * s[1],
+                             static_cast<float>(acc[2]) * hs * s[2], static_cast<float>(acc[3]) * hs * s[3]};
+          few_put16(to + slot * 8, __builtin_bit_cast(i32x4_t, v));
         };
         if ((l16 & 7) < m_lane) put(acc0, slot0);
         if ((l16 & 7) + 8 < m_lane) put(acc1, slot1);
       }
     }
   };
-  const int rd = l16 * 128, sw = l16 & 7;
   for (int i = 0, slot = 0; i < total; ++i) {
     if (st == 0) begin(ju);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (D - 1)) : "memory");
-    const uint8_t* at = ring + slot * 2048 + rd;
-    const i32x4_t w0 = *reinterpret_cast<const i32x4_t*>(at + ((kg ^ sw) * 16));
-    const i32x4_t w1 = *reinterpret_cast<const i32x4_t*>(at + (((4 + kg) ^ sw) * 16));
+    few_wait<D - 1>();
+    i32x4_t w0, w1;
+    few_read(ring + slot * kFewSlot, w0, w1);
     // past k the weights are zeros, and any codes will do
     const int k0 = min(st * kFewStep + kg * 16, K - 16), k1 = min(st * kFewStep + 64 + kg * 16, K - 16);
     const i32x4_t a0 = *reinterpret_cast<const i32x4_t*>(x0 + k0), a1 = *reinterpret_cast<const i32x4_t*>(x0 + k1);
@@ -479,7 +390,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
   // no load to LDS outlives the block
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   if constexpr (KIND == 1) {
-    __syncthreads();
+    few_barrier();
     // out[t] = residual[t] + sum_j w[t, j] y[t k + j], in increasing j
     const int my_tiles = (tiles - b + kFewBlocks - 1) / kFewBlocks;
     for (int i = tid; i < my_tiles * a.T; i += kFewThreads) {

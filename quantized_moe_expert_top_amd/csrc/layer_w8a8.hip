@@ -97,7 +97,7 @@ Ws carve(void* base, int T, int H, int I, int E, int k) {
 // kernel y of the block's tiles.
 template <int D>
 size_t few_lds(int kind, int T, int H, int I, int k) {
-  const size_t ring = kFewWaves * D * 2048, R = static_cast<size_t>(T) * k;
+  const size_t ring = kFewWaves * D * kFewSlot, R = static_cast<size_t>(T) * k;
   if (kind == 0) return ring + static_cast<size_t>(T) * (H + 16);
   return ring + R * (I + 16) + static_cast<size_t>((H / 8 + kFewBlocks - 1) / kFewBlocks) * R * 32;
 }

@@ -4,6 +4,7 @@
 // 16-bit values, so the choice of a kernel is theirs for that K.
 #include "launch_block.h"
 #include "launch_int8.h"
+#include "linear_few.h"
 #include "mm_few.h"
 #include "mm_launch.h"
 
@@ -47,7 +48,53 @@ hipError_t launch_grouped_i8(const GroupedI8& g, hipStream_t s) {
   return launch<i8_tag<bf16_tag>>(a, mm_forward_plan(g.rows, g.E, g.N, g.K / 2, a.act), s, false);
 }
 
+// ---- up to 16 rows: linear_few.h
+namespace {
+
+// LDS of linear_few_kernel beside its static arrays: 8 tiles of 16 x 17 sums and the rows' scales
+constexpr int kLinearLds = 160 * 1024 - 9216;
+inline long long linear_lds(int depth, int rows, int K) {
+  return static_cast<long long>(kFewWaves) * depth * kFewSlot + static_cast<long long>(rows) * (K + 16);
+}
+template <bool VALUES, class XT, class O, bool OUT32, int D>
+hipError_t few_go(const LinearI8& l, const void* x, hipStream_t s) {
+  auto* kern = &linear_few_kernel<VALUES, XT, O, OUT32, D>;
+  static MMReady ready;
+  const hipError_t e = ready.set(reinterpret_cast<const void*>(kern), kLinearLds);
+  if (e != hipSuccess) return e;
+  const int tiles = l.act == kActSwiglu ? (l.N / 2 + 7) / 8 : (l.N + 15) / 16;
+  hipLaunchKernelGGL(kern, dim3(tiles < kFewBlocks ? tiles : kFewBlocks), dim3(kFewThreads),
+                     static_cast<size_t>(linear_lds(D, l.rows, l.K)), s, l, x);
+  return hipGetLastError();
+}
+template <bool VALUES, class XT, class O, bool OUT32>
+hipError_t few_depth(const LinearI8& l, const void* x, hipStream_t s) {
+  if (linear_lds(8, l.rows, l.K) <= kLinearLds) return few_go<VALUES, XT, O, OUT32, 8>(l, x, s);
+  return few_go<VALUES, XT, O, OUT32, 4>(l, x, s);
+}
+template <bool VALUES, class XT>
+hipError_t few_out(const LinearI8& l, const void* x, hipStream_t s) {
+  if (l.y_type == 2) return few_depth<VALUES, XT, bf16_tag, true>(l, x, s);
+  return l.y_type == 1 ? few_depth<VALUES, XT, fp16_tag, false>(l, x, s)
+                       : few_depth<VALUES, XT, bf16_tag, false>(l, x, s);
+}
+bool few_rows(const LinearI8& l) {
+  const long long tiles = l.act == kActSwiglu ? l.N / 16 : (l.N + 15) / 16;
+  return l.rows <= kFewTokens && tiles <= static_cast<long long>(kFewBlocks) * kLinearTiles &&
+         linear_lds(4, l.rows, l.K) <= kLinearLds;
+}
+
+}  // namespace
+
+bool linear_w8a8_makes_codes(const LinearI8& l) {
+  return few_rows(l) && static_cast<long long>(l.rows) * l.K <= kFewValues;
+}
+hipError_t launch_linear_w8a8_values(const LinearI8& l, const void* x, int x_type, hipStream_t s) {
+  return x_type == 1 ? few_out<true, fp16_tag>(l, x, s) : few_out<true, bf16_tag>(l, x, s);
+}
+
 hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
+  if (few_rows(l)) return check ? hipSuccess : few_out<false, bf16_tag>(l, nullptr, s);
   MMArgs a = {};
   a.A = l.q;
   a.B = l.w;
