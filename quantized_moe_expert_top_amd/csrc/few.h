@@ -48,7 +48,7 @@ __device__ __forceinline__ void few_add(int* p, int v) {
 constexpr int kFewChunks = 4, kFewValues = kFewChunks * 8 * kFewThreads;
 template <class T, bool F32>
 struct FewRows {
-  Vals8<T, F32> v[kFewChunks];
+  Row8<T, F32> v[kFewChunks];
   uint32_t inv;   // division by the chunks of a row, exact below 2^16
   __device__ __forceinline__ int row_of(int c) const { return __umulhi(c, inv); }
   __device__ __forceinline__ void get(const void* x, int rows, int K) {
@@ -65,7 +65,7 @@ struct FewRows {
     for (int i = 0; i < kFewChunks; ++i) {
       if (i * kFewThreads >= total) break;
       const int c = threadIdx.x + i * kFewThreads, r = row_of(min(c, total - 1));
-      const uint32_t a = v[i].amax(0);   // past the end: the last chunk again
+      const uint32_t a = amax8(v[i], 0);   // past the end: the last chunk again
       const int r0 = __builtin_amdgcn_readfirstlane(r);
       if (__ballot(r != r0) == 0) {
         const uint32_t w = wave_max_u32(a);

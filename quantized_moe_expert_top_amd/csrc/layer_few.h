@@ -427,14 +427,14 @@ __global__ __launch_bounds__(256) void layer_route_kernel(const FewArgs a, int8_
   const int C = a.H / 8;
   const size_t row = static_cast<size_t>(blockIdx.x) * a.H;
   constexpr int NC = 8;   // H <= 16384
-  Vals8<T, false> v[NC];
+  Row8<T, false> v[NC];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < NC; ++i)
     if (i * 256 < C) v[i].load(a.x, row + min(static_cast<int>(threadIdx.x) + i * 256, C - 1) * 8);
 #pragma unroll
   for (int i = 0; i < NC; ++i)
-    if (i * 256 < C) m = v[i].amax(m);
+    if (i * 256 < C) m = amax8(v[i], m);
   m = wave_max_u32(m);
   if (lane == 0) red[wv] = m;
   __syncthreads();

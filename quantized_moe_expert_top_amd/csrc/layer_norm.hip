@@ -113,40 +113,52 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float (*red)[2]) {
 }
 
 // What a thread holds of a row: a chunk of 8 of each operand, as it is stored.
+template <class T, bool R32>
 struct LnChunk {
-  float x[8];   // r'
-  uint4 d;      // dh
-  float dr[8];  // dr'
+  Row8<T, R32> x, dr;   // r', dr'
+  uint4 d;              // dh
 };
 // LATE: dr' only where it is added (rows too wide to hold it from the start)
-template <class T, bool LATE>
-__device__ __forceinline__ void ln_load(const LayerNormArgs& a, size_t at, bool in, LnChunk& v) {
-#pragma unroll
-  for (int x = 0; x < 8; ++x) v.x[x] = v.dr[x] = 0.0f;
+template <class T, bool R32, bool LATE>
+__device__ __forceinline__ void ln_load(const LayerNormArgs& a, size_t at, bool in, LnChunk<T, R32>& v) {
+  v.x.zero();
+  v.dr.zero();
   v.d = make_uint4(0, 0, 0, 0);
   if (!in) return;
-  row_load8<T>(a.r, at, a.r_f32, v.x);
+  v.x.load(a.r, at);
   v.d = ld16(static_cast<const uint16_t*>(a.dh) + at);
-  if (!LATE && a.dr_out) row_load8<T>(a.dr_out, at, a.r_f32, v.dr);
+  if (!LATE && a.dr_out) v.dr.load(a.dr_out, at);
 }
 
 // One row held by W waves (the whole block, or one wave of it): its gradient, and its
-// part of the sums over tokens.
-template <class T, int W, int NC, bool LATE, bool STREAM>
+// part of the sums over tokens. The rows' values and products stay unpacked over the three
+// phases: unpacked in each of them, the arithmetic takes as long as the memory. (Not the
+// products of rows too wide for that, NC 4.)
+template <class T, int W, int NC, bool R32, bool LATE, bool STREAM>
 __device__ __forceinline__ void ln_row(const LayerNormArgs& a, size_t row, int rt, int C, float inv_h,
-                                       const uint4 (&wt)[NC], LnChunk (&v)[NC], float (*red)[W][2],
+                                       const uint4 (&wt)[NC], LnChunk<T, R32> (&v)[NC], float (*red)[W][2],
                                        float (&sw)[NC][8], float (&sb)[NC][8]) {
   constexpr int kThr = W * kWave;
-  float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
+  constexpr bool kHold = NC < 4;
+  float x[NC][8], dw[kHold ? NC : 1][8];   // r', then r' - mean; dh w
+  auto products = [&](int i, float(&p)[8]) {
     float w[8], d[8];
     unpack8<T>(wt[i], w);
     unpack8<T>(v[i].d, d);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {   // zeros past the row
-      s1 += v[i].x[x];
-      s2 += d[x] * w[x];
+    for (int e = 0; e < 8; ++e) p[e] = d[e] * w[e];
+  };
+  float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (!kHold) __builtin_amdgcn_sched_barrier(0);   // one chunk's at a time: together they would spill
+    float(&q)[8] = dw[kHold ? i : 0];
+    v[i].x.values(x[i]);
+    products(i, q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {   // zeros past the row
+      s1 += x[i][e];
+      s2 += q[e];
     }
   }
   row_sum2<W>(s1, s2, red[0]);
@@ -154,16 +166,15 @@ __device__ __forceinline__ void ln_row(const LayerNormArgs& a, size_t row, int r
   float s3 = 0.0f, s4 = 0.0f;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    if constexpr (NC > 2) __builtin_amdgcn_sched_barrier(0);
+    if (!kHold) __builtin_amdgcn_sched_barrier(0);
     if (rt + i * kThr >= C) continue;
-    float w[8], d[8];
-    unpack8<T>(wt[i], w);
-    unpack8<T>(v[i].d, d);
+    float(&q)[8] = dw[kHold ? i : 0];
+    if (!kHold) products(i, q);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      v[i].x[x] -= mean;
-      s3 += v[i].x[x] * v[i].x[x];
-      s4 += d[x] * w[x] * v[i].x[x];
+    for (int e = 0; e < 8; ++e) {
+      x[i][e] -= mean;
+      s3 += x[i][e] * x[i][e];
+      s4 += q[e] * x[i][e];
     }
   }
   row_sum2<W>(s3, s4, red[1]);
@@ -172,28 +183,29 @@ __device__ __forceinline__ void ln_row(const LayerNormArgs& a, size_t row, int r
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = rt + i * kThr;
-    // one chunk's operands unpacked at a time: together they would spill
-    if constexpr (NC > 2) __builtin_amdgcn_sched_barrier(0);
     if (c >= C) continue;
-    float w[8], d[8];
-    if (LATE && a.dr_out) row_load8<T>(a.dr_out, row + c * 8, a.r_f32, v[i].dr);
-    unpack8<T>(wt[i], w);
+    if (!kHold) __builtin_amdgcn_sched_barrier(0);
+    float(&q)[8] = dw[kHold ? i : 0];
+    if (!kHold) products(i, q);
+    float d[8], dr[8];
+    if (LATE && a.dr_out) v[i].dr.load(a.dr_out, row + c * 8);
+    v[i].dr.values(dr);
     unpack8<T>(v[i].d, d);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float xh = v[i].x[x] * p;
-      v[i].dr[x] += p * (d[x] * w[x] - md - xh * mx);
-      sw[i][x] += d[x] * xh;
-      sb[i][x] += d[x];
+    for (int e = 0; e < 8; ++e) {
+      const float xh = x[i][e] * p;
+      dr[e] = __builtin_fmaf(p, __builtin_fmaf(-xh, mx, q[e] - md), dr[e]);
+      sw[i][e] = __builtin_fmaf(d[e], xh, sw[i][e]);
+      sb[i][e] += d[e];
     }
-    row_put8<T, STREAM>(a.dr, row + c * 8, a.r_f32, v[i].dr);
+    row_put8<T, STREAM>(a.dr, row + c * 8, R32, dr);
   }
 }
 
 // Rows blockIdx, blockIdx + grid, ...; the sums over tokens stay in registers and go to
 // part[blockIdx] at the end, joined in order afterwards. AHEAD: the next row is
 // requested before this one's reductions.
-template <class T, int W, int NC, bool AHEAD, bool STREAM>
+template <class T, int W, int NC, bool R32, bool AHEAD, bool STREAM>
 __global__ __launch_bounds__(W * 64) void layer_norm_backward_kernel(const LayerNormArgs a) {
   constexpr int kThr = W * kWave;
   __shared__ float red[2][W][2];
@@ -208,12 +220,12 @@ __global__ __launch_bounds__(W * 64) void layer_norm_backward_kernel(const Layer
 #pragma unroll
     for (int x = 0; x < 8; ++x) sw[i][x] = sb[i][x] = 0.0f;
   }
-  LnChunk v[NC], nx[NC];
-  auto request = [&](long long t, LnChunk (&to)[NC]) {
+  LnChunk<T, R32> v[NC], nx[NC];
+  auto request = [&](long long t, LnChunk<T, R32> (&to)[NC]) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = rt + i * kThr;
-      ln_load<T, !AHEAD>(a, static_cast<size_t>(t) * a.H + c * 8, c < C && t < a.T, to[i]);
+      ln_load<T, R32, !AHEAD>(a, static_cast<size_t>(t) * a.H + c * 8, c < C && t < a.T, to[i]);
     }
   };
   if constexpr (AHEAD) request(blockIdx.x, nx);
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(W * 64) void layer_norm_backward_kernel(const Layer
     } else {
       request(t, v);
     }
-    ln_row<T, W, NC, !AHEAD, STREAM>(a, static_cast<size_t>(t) * a.H, rt, C, inv_h, wt, v, red, sw, sb);
+    ln_row<T, W, NC, R32, !AHEAD, STREAM>(a, static_cast<size_t>(t) * a.H, rt, C, inv_h, wt, v, red, sw, sb);
   }
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
@@ -243,7 +255,7 @@ __global__ __launch_bounds__(W * 64) void layer_norm_backward_kernel(const Layer
 // before the end, where the waves' sums over tokens are joined in wave order.
 constexpr int kLnWaves = 8;
 
-template <class T, bool STREAM>
+template <class T, bool R32, bool STREAM>
 __global__ __launch_bounds__(kLnWaves * 64) void layer_norm_backward_wave_kernel(const LayerNormArgs a) {
   __shared__ __attribute__((aligned(16))) float join[kLnWaves - 1][512];
   const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x >> 6;
@@ -257,16 +269,13 @@ __global__ __launch_bounds__(kLnWaves * 64) void layer_norm_backward_wave_kernel
   for (long long t = static_cast<long long>(blockIdx.x) * kLnWaves + wv; t < a.T;
        t += static_cast<long long>(gridDim.x) * kLnWaves) {
     const size_t row = static_cast<size_t>(t) * a.H;
-    LnChunk v[1];
-    ln_load<T, false>(a, row + lane * 8, in, v[0]);
-    ln_row<T, 1, 1, false, STREAM>(a, row, lane, C, inv_h, wt, v, static_cast<float(*)[1][2]>(nullptr), sw, sb);
+    LnChunk<T, R32> v[1];
+    ln_load<T, R32, false>(a, row + lane * 8, in, v[0]);
+    ln_row<T, 1, 1, R32, false, STREAM>(a, row, lane, C, inv_h, wt, v, static_cast<float(*)[1][2]>(nullptr), sw, sb);
   }
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.H;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float(&s)[8] = k == 0 ? sw[0] : sb[0];
-    if (k > 0) __syncthreads();   // the sums before are read
+  auto to_part = [&](float(&s)[8], float* to) {
     if (wv > 0) row_store8<T>(join[wv - 1], static_cast<size_t>(lane) * 8, true, s);
     __syncthreads();
     if (wv == 0 && in) {
@@ -277,9 +286,12 @@ __global__ __launch_bounds__(kLnWaves * 64) void layer_norm_backward_wave_kernel
 #pragma unroll
         for (int x = 0; x < 8; ++x) s[x] += o[x];
       }
-      row_store8<T>(part, static_cast<size_t>(a.H) * k + lane * 8, true, s);
+      row_store8<T>(to, static_cast<size_t>(lane) * 8, true, s);
     }
-  }
+  };
+  to_part(sw[0], part);
+  __syncthreads();   // those sums are read
+  to_part(sb[0], part + a.H);
 }
 
 // part [blocks][2][H] -> dw, db (those that are asked for), in block order over 32 runs:
@@ -317,16 +329,20 @@ hipError_t forward(const LayerNormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class T, bool R32, bool STREAM>
+hipError_t backward_as(const LayerNormArgs& a, int blocks, hipStream_t s) {
+  const int C = a.H / 8;
+  if (C <= 64) layer_norm_backward_wave_kernel<T, R32, STREAM><<<blocks, kLnWaves * 64, 0, s>>>(a);
+  else if (C <= 128) layer_norm_backward_kernel<T, 2, 1, R32, true, STREAM><<<blocks, 128, 0, s>>>(a);
+  else if (C <= 256) layer_norm_backward_kernel<T, 4, 1, R32, true, STREAM><<<blocks, 256, 0, s>>>(a);
+  else if (C <= 512) layer_norm_backward_kernel<T, 8, 1, R32, true, STREAM><<<blocks, 512, 0, s>>>(a);
+  else if (C <= 1024) layer_norm_backward_kernel<T, 8, 2, R32, true, STREAM><<<blocks, 512, 0, s>>>(a);
+  else layer_norm_backward_kernel<T, 8, 4, R32, false, STREAM><<<blocks, 512, 0, s>>>(a);
+  return hipGetLastError();
+}
 template <class T, bool STREAM>
 hipError_t backward(const LayerNormArgs& a, int blocks, hipStream_t s) {
-  const int C = a.H / 8;
-  if (C <= 64) layer_norm_backward_wave_kernel<T, STREAM><<<blocks, kLnWaves * 64, 0, s>>>(a);
-  else if (C <= 128) layer_norm_backward_kernel<T, 2, 1, true, STREAM><<<blocks, 128, 0, s>>>(a);
-  else if (C <= 256) layer_norm_backward_kernel<T, 4, 1, true, STREAM><<<blocks, 256, 0, s>>>(a);
-  else if (C <= 512) layer_norm_backward_kernel<T, 4, 2, true, STREAM><<<blocks, 256, 0, s>>>(a);
-  else if (C <= 1024) layer_norm_backward_kernel<T, 8, 2, true, STREAM><<<blocks, 512, 0, s>>>(a);
-  else layer_norm_backward_kernel<T, 8, 4, false, STREAM><<<blocks, 512, 0, s>>>(a);
-  return hipGetLastError();
+  return a.r_f32 ? backward_as<T, true, STREAM>(a, blocks, s) : backward_as<T, false, STREAM>(a, blocks, s);
 }
 
 // The forward's operands from row t0 on.

@@ -12,6 +12,32 @@ __device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8]) {
   unpack2<T>(p.z, v[4], v[5]);
   unpack2<T>(p.w, v[6], v[7]);
 }
+// Eight values of a row as they are stored: 16 bytes of T, or 32 of float32.
+template <class T, bool F32>
+struct Row8 {
+  uint4 lo, hi;   // hi: float32 only
+  __device__ __forceinline__ void load(const void* x, size_t at) {
+    if constexpr (F32) {
+      lo = ld16(static_cast<const float*>(x) + at);
+      hi = ld16(static_cast<const float*>(x) + at + 4);
+    } else {
+      lo = ld16(static_cast<const uint16_t*>(x) + at);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+    lo = make_uint4(0, 0, 0, 0);
+    hi = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (F32) {
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+      unpack8<T>(lo, v);
+    }
+  }
+};
 template <class T>
 __device__ __forceinline__ void row_load8(const void* p, size_t at, bool f32, float (&v)[8]) {
   if (f32) {

@@ -3,60 +3,35 @@
 // q = 0; a row with an infinity or a NaN has s = NaN and q = 0, so that every product
 // of it is NaN.
 #pragma once
-#include "mm.h"
+#include "norm_rows.h"
 
 namespace moe {
 
 // max|x| travels as the bits of |x|, which order as the values do, with infinities and
 // NaN above them: no value is dropped, as fmaxf drops NaN.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// Eight values of a row as they are stored: 16 bytes of T, or 32 of float32.
+// The largest |x| of eight values as float32 bits. 16-bit values are compared as they are
+// stored, two at a time.
 template <class T, bool F32>
-struct Vals8 {
-  uint4 lo, hi;   // hi: float32 only
-  __device__ __forceinline__ void load(const void* x, size_t at) {
-    if constexpr (F32) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at);
-      lo = p[0];
-      hi = p[1];
-    } else {
-      lo = ld16(static_cast<const uint16_t*>(x) + at);
-    }
-  }
-  // the largest |x| as float32 bits. 16-bit values are compared as they are, two at a time.
-  __device__ __forceinline__ uint32_t amax(uint32_t m) const {
-    if constexpr (F32) {
-      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+__device__ __forceinline__ uint32_t amax8(const Row8<T, F32>& x, uint32_t m) {
+  if constexpr (F32) {
+    const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_u32(m, w[i] & 0x7FFFFFFFu);
-      return m;
-    } else {
-      typedef __attribute__((__vector_size__(2 * sizeof(uint16_t)))) uint16_t u16x2_t;
-      auto mx = [](uint32_t a, uint32_t b) {
-        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
-                                                                      __builtin_bit_cast(u16x2_t, b)));
-      };
-      const uint32_t w = mx(mx(lo.x & 0x7FFF7FFFu, lo.y & 0x7FFF7FFFu), mx(lo.z & 0x7FFF7FFFu, lo.w & 0x7FFF7FFFu));
-      float a, b;
-      unpack2<T>(max_u32(w & 0xFFFFu, w >> 16), a, b);
-      return max_u32(m, __float_as_uint(a));
-    }
+    for (int i = 0; i < 8; ++i) m = max_u32(m, w[i] & 0x7FFFFFFFu);
+    return m;
+  } else {
+    typedef __attribute__((__vector_size__(2 * sizeof(uint16_t)))) uint16_t u16x2_t;
+    auto mx = [](uint32_t a, uint32_t b) {
+      return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                    __builtin_bit_cast(u16x2_t, b)));
+    };
+    const uint32_t w = mx(mx(x.lo.x & 0x7FFF7FFFu, x.lo.y & 0x7FFF7FFFu), mx(x.lo.z & 0x7FFF7FFFu, x.lo.w & 0x7FFF7FFFu));
+    float a, b;
+    unpack2<T>(max_u32(w & 0xFFFFu, w >> 16), a, b);
+    return max_u32(m, __float_as_uint(a));
   }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    if constexpr (F32) {
-      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
-      unpack2<T>(lo.x, v[0], v[1]);
-      unpack2<T>(lo.y, v[2], v[3]);
-      unpack2<T>(lo.z, v[4], v[5]);
-      unpack2<T>(lo.w, v[6], v[7]);
-    }
-  }
-};
+}
 
 struct RowScale {
   float s, r;   // the scale, and about 1 / s (0 where every code is 0, infinite where s is

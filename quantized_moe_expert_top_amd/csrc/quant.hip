@@ -18,12 +18,12 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void quant_rows_kernel(
   if (t >= rows) return;   // whole waves; with WPR > 1, whole blocks
   const int C = K / 8;
   const size_t row = static_cast<size_t>(t) * K;
-  Vals8<T, F32> v[NC];
+  Row8<T, F32> v[NC];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < NC; ++i) v[i].load(x, row + min(rt + i * kRowThreads, C - 1) * 8);   // past the row: its last
 #pragma unroll
-  for (int i = 0; i < NC; ++i) m = v[i].amax(m);
+  for (int i = 0; i < NC; ++i) m = amax8(v[i], m);
   m = wave_max_u32(m);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x >> 6] = m;
