@@ -90,9 +90,10 @@ __device__ __forceinline__ int few_table_wave(int id, int R, uint16_t* act, uint
 }
 
 // The picked experts in ascending order: expert act[i] has the slots sorted[beg[i]] to
-// sorted[beg[i + 1]]. Their order is free: it only says which column of a product a slot
-// takes. Returns the number of experts. ids in LDS, behind a barrier; count: 1024 words of
-// LDS that nothing else uses. All threads.
+// sorted[beg[i + 1]], ascending up to 64 slots. Past 64 their order depends on timing (here
+// it only says which column of a product a slot takes), and count[e] is beg of expert e.
+// Returns the number of experts. ids in LDS, behind a barrier; count: 1024 words of LDS that
+// nothing else uses. All threads.
 __device__ __forceinline__ int few_table(const int* ids, int R, int* count, uint16_t* act, uint16_t* beg, uint16_t* sorted) {
   const int f = threadIdx.x, lane = f & (kWave - 1);
   if (R <= kWave) return few_table_wave(lane < R ? ids[lane] : -1, R, act, beg, sorted);

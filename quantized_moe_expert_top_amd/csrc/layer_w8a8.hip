@@ -1,6 +1,6 @@
 // The whole routed layer on int8 weights in one call (moe_layer_w8a8).
 #include "launch.h"
-#include "layer_few.h"
+#include "layer_rows.h"
 #include "launch_int8.h"
 #include "mm_launch.h"
 #include "norm_rows.h"
@@ -9,7 +9,8 @@ namespace moe {
 namespace {
 
 // out[t] = residual[t] + sum_j w[t, j] y[slot_pos[t k + j]] in increasing j, 8 columns
-// a thread (combine.hip, with a residual and the type of the results).
+// a thread (combine.hip, with a residual and the type of the results). slot_pos NULL: y is
+// by slot.
 template <class T, bool F32>
 __global__ __launch_bounds__(256) void combine_out_kernel(const float* __restrict__ y,
                                                           const int* __restrict__ slot_pos,
@@ -30,7 +31,7 @@ __global__ __launch_bounds__(256) void combine_out_kernel(const float* __restric
     for (int u = 0; u < kJB; ++u) {   // past the last pick: the last again, unused
       const int j = t * k + min(j0 + u, k - 1);
       wj[u] = w[j];
-      row_load8<T>(y, static_cast<size_t>(slot_pos[j]) * H + c * 8, true, v[u]);
+      row_load8<T>(y, static_cast<size_t>(slot_pos ? slot_pos[j] : j) * H + c * 8, true, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kJB; ++u)
@@ -65,6 +66,7 @@ struct Ws {
   float* hs;
   float* y;
   FewRecord* record;
+  RowsRecord* rows_record;
   size_t total;
 };
 Ws carve(void* base, int T, int H, int I, int E, int k) {
@@ -89,6 +91,7 @@ Ws carve(void* base, int T, int H, int I, int E, int k) {
   w.hs = reinterpret_cast<float*>(take(R * 4));
   w.y = reinterpret_cast<float*>(take(R * H * 4));
   w.record = reinterpret_cast<FewRecord*>(take(sizeof(FewRecord)));
+  w.rows_record = reinterpret_cast<RowsRecord*>(take(sizeof(RowsRecord)));
   w.total = at;
   return w;
 }
@@ -143,6 +146,35 @@ bool few_fits(int T, int H, int I, int k) {
   return T <= kFewTokens && few_lds<2>(0, T, H, I, k) <= size_t{kFewLds} && few_lds<2>(1, T, H, I, k) <= size_t{kFewLds};
 }
 
+// Up to 512 picks: those whose codes do not fit in LDS, and more than 16 tokens while
+// experts rarely have more than the 16 rows of a unit. 64 tokens x 4096 x 1536, 32 experts
+// against tiles: 4 picks (8 an expert) 127 us against 140; 16 experts (16 an expert) 94.5
+// against 87.9. 2048 x 768 x 128 experts, 8 of them: 93 against 113 (24 of 64 tokens and
+// fewer: 70 to 81 against 85 to 98). At 8 an expert seven sizes lie between 12 percent
+// better and 8 worse.
+bool rows_fit(int T, int E, int k) {
+  const int R = T * k;
+  return T <= kFewMaxR && R <= kFewMaxR && (T <= kFewTokens || R <= 8 * E);
+}
+template <int KIND>
+hipError_t rows_go(const RowsArgs& a, hipStream_t s) {
+  constexpr int kLds = kFewWaves * kRowsDepth * kRowsSlot;
+  auto* kern = &layer_rows_kernel<KIND>;
+  static MMReady ready;
+  const hipError_t e = ready.set(reinterpret_cast<const void*>(kern), kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(kFewBlocks), dim3(kFewThreads), kLds, s, a);
+  return hipGetLastError();
+}
+template <class T>
+hipError_t route(const FewArgs& a, Ws& w, hipStream_t s) {
+  const unsigned blocks = a.T + (a.T + 3) / 4;
+  if (a.E <= 128) layer_route_kernel<T, 2><<<blocks, 256, 0, s>>>(a, w.xq, w.xs);
+  else if (a.E <= 256) layer_route_kernel<T, 4><<<blocks, 256, 0, s>>>(a, w.xq, w.xs);
+  else layer_route_kernel<T, 16><<<blocks, 256, 0, s>>>(a, w.xq, w.xs);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t layer_w8a8_workspace_bytes(int T, int H, int I, int E, int k) {
@@ -153,13 +185,25 @@ hipError_t launch_layer_w8a8(const LayerI8& l, void* base, hipStream_t s) {
   const int T = l.T, H = l.H, I = l.I, E = l.E, k = l.k;
   Ws w = carve(base, T, H, I, E, k);
   if (l.offsets) w.offsets = l.offsets;
+  const FewArgs few = {l.logits, l.x, w.xq, w.xs, w.hq, w.hs, l.w13, l.s13, l.w2, l.s2, l.residual, l.ids, l.w,
+                       l.offsets, w.record, w.h, l.out, T, H, I, E, k};
   if (T > 0 && few_fits(T, H, I, k)) {
-    const FewArgs a = {l.logits, l.x, w.xq, w.xs, w.hq, w.hs, l.w13, l.s13, l.w2, l.s2, l.residual, l.ids, l.w, l.offsets, w.record, w.h, l.out,
-                       T, H, I, E, k};
-    const hipError_t e = l.x_type == 1 ? few_up<fp16_tag>(a, s) : few_up<bf16_tag>(a, s);
+    const hipError_t e = l.x_type == 1 ? few_up<fp16_tag>(few, s) : few_up<bf16_tag>(few, s);
     if (e != hipSuccess) return e;
-    return l.out_type == 2 ? few_down<bf16_tag, true>(a, s)
-         : l.out_type == 1 ? few_down<fp16_tag, false>(a, s) : few_down<bf16_tag, false>(a, s);
+    return l.out_type == 2 ? few_down<bf16_tag, true>(few, s)
+         : l.out_type == 1 ? few_down<fp16_tag, false>(few, s) : few_down<bf16_tag, false>(few, s);
+  }
+  if (T > 0 && rows_fit(T, E, k)) {
+    const int R = T * k;
+    hipError_t e = l.x_type == 1 ? route<fp16_tag>(few, w, s) : route<bf16_tag>(few, w, s);
+    if (e != hipSuccess) return e;
+    e = rows_go<0>({w.xq, w.xs, l.w13, l.s13, l.ids, w.h, l.offsets, w.rows_record, T, R, H, I, E, k}, s);
+    if (e != hipSuccess) return e;
+    e = launch_quant_rows(w.h, 2, R, I, w.hq, w.hs, s);
+    if (e != hipSuccess) return e;
+    e = rows_go<1>({w.hq, w.hs, l.w2, l.s2, l.ids, w.y, nullptr, w.rows_record, R, R, I, H, E, k}, s);
+    if (e != hipSuccess) return e;
+    return launch_combine_out(w.y, nullptr, l.w, l.residual, T, H, k, l.out, l.out_type, s);
   }
   hipError_t e = launch_route_topk(l.logits, T, E, k, l.ids, l.w, s);
   if (e != hipSuccess) return e;

@@ -251,7 +251,8 @@ SHAPES = [(1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (2, 2048, 768, 128, 8), (2, 14
           (3, 1040, 272, 40, 3), (4, 512, 256, 64, 8), (4, 7168, 64, 16, 4), (5, 528, 400, 130, 6),
           (8, 2064, 784, 32, 2), (13, 1024, 512, 300, 8), (16, 2048, 768, 128, 8), (17, 320, 160, 12, 4),
           (33, 256, 176, 7, 3), (64, 1024, 384, 128, 8), (100, 256, 128, 4, 1), (1, 64, 2048, 600, 32),
-          (2, 48, 32, 1024, 16), (16, 16, 16, 2, 1), (300, 512, 256, 64, 8)]
+          (2, 48, 32, 1024, 16), (16, 16, 16, 2, 1), (300, 512, 256, 64, 8), (16, 8192, 1040, 16, 4),
+          (12, 16384, 16, 3, 2), (50, 2064, 272, 64, 10), (64, 80, 48, 1000, 8), (512, 64, 32, 64, 1)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", SHAPES)
