@@ -110,7 +110,12 @@ hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
   a.kdim = l.K / 2;
   a.act = l.act;
   a.c_f32 = l.y_type == 2;
-  const int plan = mm_forward_plan(l.rows, 0, l.N, l.K / 2, l.act);
+  int plan = mm_forward_plan(l.rows, 0, l.N, l.K / 2, l.act);
+  // Two tiles of 32 rows over all CUs and more: their second round takes as long as the
+  // first, however few rows it has (33 x 4096 x 7168, SwiGLU: 22.8 us, tiles of 64 x 64
+  // 14.2; 32 rows, one tile: 13.1 against 13.3).
+  if (plan == 7 && l.rows > 32 && mm_row_tiles(32, l.rows, 0) * ((l.N + 15) / 16) > kFewBlocks)
+    plan = mm_pick_rows(l.rows, 0, l.N, l.K / 2, l.act).geom;
   return l.y_type == 1 ? launch<i8_tag<fp16_tag>>(a, plan, s, check)
                        : launch<i8_tag<bf16_tag>>(a, plan, s, check);
 }

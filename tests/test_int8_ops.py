@@ -176,7 +176,8 @@ def test_every_kernel_gated(M, K, N, name):
 # one launch up to 16384 values; 8 tiles to a block; rows in LDS; and the kernel past them
 @pytest.mark.parametrize("M,K,N", [(16, 1024, 272), (16, 1040, 272), (1, 16384, 32), (1, 65536, 64), (2, 65536, 64),
                                    (16, 8192, 144), (16, 16384, 48), (3, 272, 8208), (2, 64, 32768), (2, 64, 32784),
-                                   (9, 48, 32000), (17, 6160, 56), (29, 1040, 2056), (32, 2048, 2048)])
+                                   (9, 48, 32000), (17, 6160, 56), (29, 1040, 2056), (32, 2048, 2048),
+                                   (32, 7168, 2064), (33, 7168, 2064)])
 @pytest.mark.parametrize("act,out,by_codes", [("none", BF, False), ("swiglu", F32, True), ("silu", HF, True)])
 def test_few_rows_limits(M, K, N, act, out, by_codes):
     run_linear(M, K, N // 16 * 16 if act == "swiglu" else N, act, HF, out, K < 8192, True, by_codes, M + N)
