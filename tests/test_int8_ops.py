@@ -314,6 +314,31 @@ def test_layer_zero_and_bad_tokens(T):
     assert torch.equal(o[3:], good[3:])
 
 
+@pytest.mark.parametrize("T,E", [(2, 16), (13, 48), (16, 600), (40, 32), (90, 16)])
+def test_layer_with_bad_logits(T, E):
+    """Rows of logits without an order: route_topk's picks, all of them experts; no other
+    token changes by a bit."""
+    p, k = make_layer(T, 256, 128, E, T), 4
+    _, _, good, _ = run_layer(p, k, F32)
+    good = good.clone()
+    p["logits"][0] = float("nan")
+    bad = [0]
+    if T > 2:
+        p["logits"][3] = float("-inf")
+        p["logits"][5, ::2] = float("nan")
+        p["logits"][7] = float("inf")
+        bad += [3, 5, 7]
+    ids, w, o, off = run_layer(p, k, F32, offsets=True)
+    rid, rw = torch.empty_like(ids), torch.empty_like(w)
+    moe.route_topk(p["logits"], k, rid, rw)
+    assert torch.equal(ids, rid) and torch.equal(w.view(torch.int32), rw.view(torch.int32))
+    assert int(ids.min()) >= 0 and int(ids.max()) < E
+    counts = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    assert torch.equal(off.long(), torch.cat([counts.new_zeros(1), counts.cumsum(0)]))
+    rest = [t for t in range(T) if t not in bad]
+    assert torch.equal(o[rest], good[rest])
+
+
 def test_layer_is_the_separate_calls():
     """The picks and weights of route_topk, and the sums of the separate calls."""
     for T in (2, 12, 80):
