@@ -172,6 +172,12 @@ def test_every_kernel_gated(M, K, N, name):
     run_linear(M, K, N // 16 * 16, "swiglu", HF, HF, True, True, True, M + 1)
 
 
+@pytest.mark.parametrize("M,K,N,name", PLANS)
+@pytest.mark.parametrize("act,out", [("relu", F32), ("swiglu", HF)])
+def test_every_kernel_adds_in_place(M, K, N, name, act, out):
+    run_linear(M, K, N // 16 * 16, act, HF, out, False, True, True, M + 2, in_place=True)
+
+
 # sizes around those where the kernel of few rows begins and ends: codes made in the call's
 # one launch up to 16384 values; 8 tiles to a block; rows in LDS; and the kernel past them
 @pytest.mark.parametrize("M,K,N", [(16, 1024, 272), (16, 1040, 272), (1, 16384, 32), (1, 65536, 64), (2, 65536, 64),
@@ -396,6 +402,42 @@ def test_layer_in_a_graph(T):
         torch.cuda.synchronize()
         for a, b in zip(got, (ids, w, o)):
             assert torch.equal(a, b)
+
+
+def test_two_graphs_on_one_workspace():
+    """Nothing is kept in a workspace between calls: two graphs that share one, replayed in
+    turn, give what each gives alone."""
+    H, I, E, k = 512, 256, 32, 4
+    rows = (3, 40, 150)   # the layer's three ways
+    n = moe.layer_w8a8_workspace(max(rows), H, I, E, k)
+    ws = torch.empty(max(n, moe.linear_w8a8_workspace(max(rows), H)), dtype=torch.uint8, device=DEV)
+    runs = []
+    for T in rows:
+        p = make_layer(T, H, I, E, 40 + T)
+        ids = torch.empty((T, k), dtype=torch.int32, device=DEV)
+        w, o = torch.empty((T, k), device=DEV), torch.empty((T, H), device=DEV, dtype=BF)
+        y = torch.empty((T, 2 * I), device=DEV)
+
+        def call(p=p, ids=ids, w=w, o=o, y=y):
+            moe.linear_w8a8(p["x"], p["w13"][0], p["s13"][0], y, ws=ws)
+            moe.layer_w8a8(p["logits"], p["x"], p["w13"], p["s13"], p["w2"], p["s2"], ids, w, o, ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((p, o, y, call, g))
+    for i in range(3):
+        for p, *_ in runs:
+            p["x"].copy_(randn(gen(90 + i), p["x"].shape, BF))
+        for *_, g in runs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = [(o.clone(), y.clone()) for _, o, y, *_ in runs]
+        for (_, o, y, call, _), (go, gy) in zip(runs, got):
+            call()
+            torch.cuda.synchronize()
+            assert torch.equal(o, go) and torch.equal(y, gy)
 
 
 def test_two_streams_at_once():
