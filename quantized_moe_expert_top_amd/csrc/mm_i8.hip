@@ -1,7 +1,9 @@
 // Forward products of int8 operands (moe_linear_w8a8): y = act(z) + residual with
 // z = (sum_k q_tk w_nk) s_t u_n + b_n, on the tile and few-row kernels of the 16-bit
 // products (mm.h, mm_few.h). Bytes and matrix time of K codes are those of K / 2
-// 16-bit values, so the choice of a kernel is theirs for that K.
+// 16-bit values, so the choice of a kernel is theirs for that K. 8192 x 7168 -> SwiGLU
+// 4096: 206 us, 2.33 POP/s, bound by the matrix pipes and the clock under their load (a
+// plain library product of these sizes reaches 2.18, 16384^2 x 8192 2.41).
 #include "launch_block.h"
 #include "launch_int8.h"
 #include "linear_few.h"
