@@ -61,49 +61,18 @@ struct FewArgs {
   int T, H, I, E, k;
 };
 
-__device__ __forceinline__ void few_wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-// few_table for R <= 64 slots, whose ids the lanes hold (-1 past R): each wave by itself,
-// all writing the same values, so that no barrier is needed.
-__device__ __forceinline__ int few_table_wave(int id, int R, uint16_t* act, uint16_t* beg, uint16_t* sorted) {
-  const int f = threadIdx.x & (kWave - 1);
-  int less = 0, same = 0;
-  for (int g = 0; g < R; ++g) {
-    const int o = __builtin_amdgcn_readlane(id, g);
-    less += o < id;
-    same += o == id && g < f;
-  }
-  const uint64_t first = __ballot(f < R && same == 0);
-  int rank = 0;
-  for (uint64_t m = first; m != 0; m &= m - 1) rank += __builtin_amdgcn_readlane(id, __builtin_ctzll(m)) < id;
-  const int total = __popcll(first);
-  if (f < R) {
-    sorted[less + same] = f;
-    if (same == 0) {
-      act[rank] = id;
-      beg[rank] = less;
-    }
-  }
-  if (f == 0) beg[total] = R;
-  few_wave_sync();
-  return total;
-}
-
+__device__ __forceinline__ void few_clear(int* count) { count[threadIdx.x] = count[threadIdx.x + kFewThreads] = 0; }
 // The picked experts in ascending order: expert act[i] has the slots sorted[beg[i]] to
-// sorted[beg[i + 1]], ascending up to 64 slots. Past 64 their order depends on timing (here
-// it only says which column of a product a slot takes), and count[e] is beg of expert e.
-// Returns the number of experts. ids in LDS, behind a barrier; count: 1024 words of LDS that
-// nothing else uses. All threads.
-__device__ __forceinline__ int few_table(const int* ids, int R, int* count, uint16_t* act, uint16_t* beg, uint16_t* sorted) {
-  const int f = threadIdx.x, lane = f & (kWave - 1);
-  if (R <= kWave) return few_table_wave(lane < R ? ids[lane] : -1, R, act, beg, sorted);
+// sorted[beg[i + 1]], in an order that depends on timing (here it only says which column of
+// a product a slot takes); count[e] is beg of expert e. offsets, where given: moe_permute's.
+// Returns the number of experts. ids in LDS and few_clear(count), both behind a barrier;
+// count: 1024 words of LDS that nothing else uses. All threads, also for the few slots that a wave could order by itself:
+// one slot after another that took 2 us more at 32 slots and 4 at 64.
+__device__ __forceinline__ int few_table(const int* ids, int R, int* count, uint16_t* act, uint16_t* beg, uint16_t* sorted,
+                                         int* offsets, int E) {
+  const int f = threadIdx.x;
   static_assert(MOE_MAX_EXPERTS == 2 * kFewThreads && kFewMaxR <= kFewThreads, "a thread's experts and slots");
   __shared__ int tot[kFewWaves];
-  count[f] = count[f + kFewThreads] = 0;
-  __syncthreads();
   const int id = f < R ? ids[f] : 0;
   const int place = f < R ? atomicAdd(&count[id], 1) : 0;
   __syncthreads();
@@ -111,6 +80,11 @@ __device__ __forceinline__ int few_table(const int* ids, int R, int* count, uint
   // experts in the high half, slots in the low one
   int total;
   int at = block_excl_scan<kFewThreads>(((c0 > 0) + (c1 > 0)) << 16 | (c0 + c1), tot, total);
+  if (offsets) {
+    if (2 * f < E) offsets[2 * f] = at & 0xFFFF;
+    if (2 * f + 1 < E) offsets[2 * f + 1] = (at & 0xFFFF) + c0;
+    if (f == 0) offsets[E] = R;
+  }
   auto enter = [&](int e, int c) {
     if (c > 0) {
       act[at >> 16] = e;
@@ -126,16 +100,6 @@ __device__ __forceinline__ int few_table(const int* ids, int R, int* count, uint
   if (f < R) sorted[count[id] + place] = f;
   __syncthreads();
   return total >> 16;
-}
-
-// The picks' counts per expert as offsets (moe_permute's), by one block, from few_table's
-// list.
-__device__ __forceinline__ void few_offsets(const uint16_t* act, const uint16_t* beg, int n, int R, int E, int* offsets) {
-  for (int e = threadIdx.x; e <= E; e += kFewThreads) {
-    int i = 0;   // experts below e
-    for (int j = 0; j < n; ++j) i += act[j] < e;
-    offsets[e] = beg[i];
-  }
 }
 
 // Eight scales at each of two uniform addresses, by scalar loads: a vector load's wait
@@ -191,6 +155,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
   }
   int n_act;
   if constexpr (KIND == 0) {
+    int* count = reinterpret_cast<int*>(few_lds);   // the rings are not in use yet
+    few_clear(count);
     if constexpr (CODES) {
       if (tid < R) s_ids[tid] = a.ids[tid];
       copied.get(a.xq, a.xs, rows, K);
@@ -202,13 +168,13 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_few_kernel(const FewArgs
       made.amax(rows, K, s_amax);
     }
     few_barrier();
-    n_act = few_table(s_ids, R, reinterpret_cast<int*>(few_lds), s_act, s_beg, s_sorted);
+    n_act = few_table(s_ids, R, count, s_act, s_beg, s_sorted,
+                      blockIdx.x == 0 ? a.offsets : nullptr, a.E);
     if (blockIdx.x == 0) {
       if (!CODES && tid < R) {
         a.ids[tid] = s_ids[tid];
         a.w[tid] = s_w[tid];
       }
-      if (a.offsets) few_offsets(s_act, s_beg, n_act, R, a.E, a.offsets);
       a.record->put(n_act, R, s_act, s_beg, s_sorted);
     }
   } else {

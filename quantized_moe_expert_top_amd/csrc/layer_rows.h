@@ -54,23 +54,21 @@ __global__ __launch_bounds__(kFewThreads, 2) void layer_rows_kernel(const RowsAr
     uint16_t* s_act = reinterpret_cast<uint16_t*>(s_count + MOE_MAX_EXPERTS);
     uint16_t* s_beg = s_act + kFewMaxR;
     __shared__ int tot[kFewWaves];
+    few_clear(s_count);
     if (tid < R) s_ids[tid] = a.ids[tid];
     __syncthreads();
-    const int n_act = few_table(s_ids, R, s_count, s_act, s_beg, s_sorted);
-    if (R > kWave) {
-      // The same order in every block, ascending: an expert's groups go to several of them.
-      // (few_table's order depends on timing; up to 64 slots it is ascending.)
-      int start = 0, rank = 0;
-      if (tid < R) {
-        const int id = s_ids[tid];
-        start = s_count[id];
-        for (int p = start; p < R && s_ids[s_sorted[p]] == id; ++p) rank += s_sorted[p] < tid;
-      }
-      __syncthreads();
-      if (tid < R) s_sorted[start + rank] = static_cast<uint16_t>(tid);
-      __syncthreads();
+    const int n_act = few_table(s_ids, R, s_count, s_act, s_beg, s_sorted,
+                                blockIdx.x == 0 ? a.offsets : nullptr, a.E);
+    // the same order in every block, ascending: an expert's groups go to several of them
+    int start = 0, rank = 0;
+    if (tid < R) {
+      const int id = s_ids[tid];
+      start = s_count[id];
+      for (int p = start; p < R && s_ids[s_sorted[p]] == id; ++p) rank += s_sorted[p] < tid;
     }
-    if (blockIdx.x == 0 && a.offsets) few_offsets(s_act, s_beg, n_act, R, a.E, a.offsets);
+    __syncthreads();
+    if (tid < R) s_sorted[start + rank] = static_cast<uint16_t>(tid);
+    __syncthreads();
     const int lo = tid < n_act ? s_beg[tid] : 0, n = tid < n_act ? s_beg[tid + 1] - lo : 0;
     int at = block_excl_scan<kFewThreads>((n + 15) / 16, tot, groups);
     for (int i = 0; i < n; i += 16, ++at) {
