@@ -189,6 +189,31 @@ def test_few_rows_limits(M, K, N, act, out, by_codes):
     run_linear(M, K, N // 16 * 16 if act == "swiglu" else N, act, HF, out, K < 8192, True, by_codes, M + N)
 
 
+@pytest.mark.parametrize("M,K,N,act", [(40003, 65536, 16, "none"), (140003, 32, 16384, "relu"), (70003, 65536, 32, "swiglu")])
+def test_arrays_past_32_bits(M, K, N, act):
+    """Offsets of x, its codes and y past 2^31 and 2^32: rows at the ends and around them."""
+    g = gen(M)
+    w, u = weights(g, (N, K)), scales(g, (N,), K)
+    q = torch.empty((M, K), dtype=torch.int8, device=DEV).random_(-127, 128, generator=g)
+    sc = torch.rand((M,), generator=g, device=DEV) * 0.01
+    y = torch.full((M, N // 2 if act == "swiglu" else N), 3.0, dtype=BF, device=DEV)
+    moe.linear_w8a8(q, w, u, y, x_scale=sc, act=act)
+    at = sorted({0, 1, M - 1, M - 2, *(min(b // n + d, M - 1) for b in (2 ** 31, 2 ** 32)
+                                       for n in (K, N) for d in (0, 1))})
+    v, e = ref.linear(q[at].double(), sc[at], w, u, None, None, act, BF)
+    close(y[at], v, e, (M, K, N, act))
+
+
+def test_codes_of_rows_past_32_bits():
+    M, K = 66001, 65536
+    x = torch.empty((M, K), dtype=BF, device=DEV).normal_(generator=gen(3))
+    q, s = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty((M,), device=DEV)
+    moe.quant_rows(x, q, s)
+    at = [0, 32767, 32768, 65535, 65536, M - 1]
+    rq, rs = ref.codes(x[at])
+    assert torch.equal(s[at], rs.float()) and torch.equal(q[at].double(), rq.double())
+
+
 def test_largest_codes():
     """Sums at the ends of 32 bits: K 65536, every product 128 * 128 (2^30)."""
     M, K, N = 2, 65536, 16
@@ -269,7 +294,8 @@ SHAPES = [(1, 16, 16, 1, 1), (1, 256, 128, 8, 2), (2, 2048, 768, 128, 8), (2, 14
           (8, 2064, 784, 32, 2), (13, 1024, 512, 300, 8), (16, 2048, 768, 128, 8), (17, 320, 160, 12, 4),
           (33, 256, 176, 7, 3), (64, 1024, 384, 128, 8), (100, 256, 128, 4, 1), (1, 64, 2048, 600, 32),
           (2, 48, 32, 1024, 16), (16, 16, 16, 2, 1), (300, 512, 256, 64, 8), (16, 8192, 1040, 16, 4),
-          (12, 16384, 16, 3, 2), (50, 2064, 272, 64, 10), (64, 80, 48, 1000, 8), (512, 64, 32, 64, 1)]
+          (12, 16384, 16, 3, 2), (50, 2064, 272, 64, 10), (64, 80, 48, 1000, 8), (512, 64, 32, 64, 1),
+          (512, 256, 128, 4, 2), (1301, 528, 272, 8, 3)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", SHAPES)
@@ -279,6 +305,17 @@ def test_layer(T, H, I, E, k, x_t):
     check_layer(p, k, x_t)
     res = randn(gen(9), (T, H), x_t)
     check_layer(p, k, x_t, residual=res, in_place=True)
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(32767, 8192, 32, 8, 8), (12288, 16384, 16, 1024, 8)])
+def test_layer_at_the_limit(T, H, I, E, k):
+    """T k H just below 2^31, with 128-row tiles and with low ones: some of the tokens."""
+    p = make_layer(T, H, I, E, 5)
+    _, _, o, off = run_layer(p, k, offsets=True)
+    assert int(off[E]) == T * k
+    at = [0, 1, T // 2, T - 2, T - 1]
+    _, _, v, bound = ref.layer(p["logits"][at], p["x"][at], p["w13"], p["s13"], p["w2"], p["s2"], k, None, BF)
+    close(o[at], v, bound, (T, H, I, E, k))
 
 
 @pytest.mark.parametrize("out", [BF, HF, F32])
