@@ -38,6 +38,11 @@ __device__ __forceinline__ void few_put16(void* p, i32x4_t v) {
 __device__ __forceinline__ void few_max(uint32_t* p, uint32_t v) {
   asm volatile("ds_max_u32 %0, %1" ::"v"(few_lds_at(p)), "v"(v) : "memory");
 }
+// An MFMA's result that inline assembly reads next. The compiler places the wait states
+// between an MFMA and the instructions it knows, but not before an asm block: the product
+// of 16x16x64 codes has 4 passes and its result may be read 8 wait states later, which the
+// branch and the address before the first such read do not fill. Once a tile, 16 of them.
+__device__ __forceinline__ void few_settle(i32x4_t& acc) { asm volatile("s_nop 15" : "+v"(acc)); }
 __device__ __forceinline__ void few_add(int* p, int v) {
   asm volatile("ds_add_u32 %0, %1" ::"v"(few_lds_at(p)), "v"(v) : "memory");
 }

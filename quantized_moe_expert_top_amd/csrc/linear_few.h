@@ -135,6 +135,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void linear_few_kernel(const Linear
     slot = slot + 1 == D ? 0 : slot + 1;
     if (++st == each) {
       // lane: row l16 of x, weight rows 4 kg + [0, 4)
+      few_settle(acc);
       if (l16 < M)
 #pragma unroll
         for (int q = 0; q < 4; ++q) few_add(&s_acc[t][l16][kg * 4 + q], acc[q]);
