@@ -66,8 +66,8 @@ class LayerBuffers:
         pws = _lib.permute_workspace(T, E, k)
         fws = {"w4a16": _lib.w4a16_workspace, "w4a8": _lib.w4a8_workspace,
                "w8a8": _lib.w8a8_workspace}[fmt](T, H, I, E, k)
-        lws = {"w4a16": _lib.layer_w4a16_workspace, "w8a8": layer_w8a8_workspace}.get(
-            fmt, lambda *_: 0)(T, H, I, E, k)
+        # W8A8: moe_layer's first call makes its workspace, which moe_forward never reads
+        lws = _lib.layer_w4a16_workspace(T, H, I, E, k) if fmt == "w4a16" else 0
         return cls(
             T, H, I, E, k, fmt,
             ids=torch.empty((T, k), **i32),
@@ -109,13 +109,16 @@ def moe_forward(b: LayerBuffers, x, logits, weights, debug=None, stream=None):
 def moe_layer(b: LayerBuffers, x, logits, weights, stream=None):
     """The same layer through the single whole-layer entry point (moe_layer_w4a16 or
     moe_layer_w8a8; fused kernels at decode sizes). Returns b.out. W8A8: of the buffers,
-    ids, w, offsets and out are written."""
+    ids, w, offsets and out are written, and the first call allocates b.layer_ws."""
     if b.fmt not in ("w4a16", "w8a8"):
         raise ValueError("moe_layer covers the W4A16 and W8A8 formats")
     w13, s13, w2, s2 = weights
     if b.fmt == "w8a8":
         import torch
         x = x.view(torch.bfloat16) if x.dtype == torch.int16 else x   # bf16 bits
+        need = layer_w8a8_workspace(b.T, b.H, b.I, b.E, b.k)
+        if b.layer_ws.numel() < need:
+            b.layer_ws = torch.empty(need, dtype=torch.uint8, device=b.out.device)
         layer_w8a8(logits, x, w13, s13, w2, s2, b.ids, b.w, b.out, b.layer_ws,
                    expert_offsets=b.offsets, stream=stream)
         return b.out
