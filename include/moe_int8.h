@@ -85,6 +85,16 @@ MOE_API moe_status moe_linear_w8a8(const moe_w8_shape* shape, const void* x, con
                                    void* stream);
 
 /*
+ * moe_linear_w8a8_plan — the kernel that a product of this shape runs on, chosen from the
+ * shape alone. Host only; for tests and tuning: the numbers may change between versions.
+ *   plan      int32 [3], written:
+ *     [0]  0 to 7 as moe_product_plan's [0]; 8 weights through rings of the waves
+ *     [1]  the depth of those rings, else 0
+ *     [2]  the codes of x: 0 given, 1 made in the product's launch, 2 in one before it
+ */
+MOE_API moe_status moe_linear_w8a8_plan(const moe_w8_shape* shape, int32_t* plan);
+
+/*
  * moe_layer_w8a8 — the whole W8A8 layer in one call: moe_route_topk's picks of
  * logits [T, E], the SwiGLU experts of moe_grouped_w8a8_ffn, and moe_combine's sum
  * added to a residual, by the definitions given there:

@@ -80,6 +80,7 @@ def _load() -> ctypes.CDLL:
             "moe_quant_rows": (INT, [P, I32, I32, I32, P, P, P]),
             "moe_linear_w8a8_workspace": (SZ, [I32, I32]),
             "moe_linear_w8a8": (INT, [w8] + [P] * 8 + [SZ, P]),
+            "moe_linear_w8a8_plan": (INT, [w8, P]),
             "moe_layer_w8a8_workspace": (SZ, [layer]),
             "moe_layer_w8a8": (INT, [layer, P, P, I32] + [P] * 9 + [I32, P, SZ, P]),
         }

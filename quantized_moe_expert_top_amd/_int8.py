@@ -10,6 +10,7 @@ from . import _block, _lib
 from ._block import _act, _done, _ext, _load
 
 EXPORTS = ("moe_quant_rows", "moe_linear_w8a8_workspace", "moe_linear_w8a8",
+           "moe_linear_w8a8_plan",
            "moe_layer_w8a8_workspace", "moe_layer_w8a8")
 
 
@@ -41,6 +42,20 @@ def linear_w8a8(x, w, w_scale, y, x_scale=None, bias=None, residual=None, act: s
     st = (_block._binding or _ext()).linear_w8a8(*args)
     if st:
         _done("moe_linear_w8a8", st, lambda: _block._binding.linear_w8a8(*args))
+
+
+_CODES = (None, "in the launch", "before it")
+
+
+def linear_w8a8_plan(rows: int, K: int, N: int, act: str = "none", codes: bool = False) -> dict:
+    """The kernel that linear_w8a8 runs on for this shape, for tests and tuning: its tiles
+    as product_plan names them, or "rings" of a depth; codes says where those of x are made
+    (None: given)."""
+    s = _block.MoeW8Shape(rows, K, N, 3 if codes else 0, 0, _act(act))
+    plan = (ctypes.c_int32 * 3)()
+    _lib._check("moe_linear_w8a8_plan", _load().moe_linear_w8a8_plan(ctypes.byref(s), plan))
+    kernel, depth, made = plan
+    return dict(kernel=(*_block._TILES, "rings")[kernel], depth=depth, codes=_CODES[made])
 
 
 def layer_w8a8_workspace(T: int, H: int, I: int, E: int, k: int) -> int:

@@ -141,7 +141,7 @@ moe_status moe_linear_w8a8(const moe_w8_shape* s, const void* x, const float* x_
   if (moe::launch_linear_w8a8(l, stm, true) != hipSuccess)
     return fail(MOE_ESHAPE, "a launch of these sizes would hold 2^32 threads or more");
   if ((st = check_device()) != MOE_OK) return st;
-  if (!codes && moe::linear_w8a8_makes_codes(l))
+  if (!codes && moe::linear_w8a8_plan(s->rows, s->K, s->N, s->act).makes_codes)
     return launched(moe::launch_linear_w8a8_values(l, x, s->x_dtype, stm), "moe_linear_w8a8 launch");
   if (!codes) {
     st = launched(moe::launch_quant_rows(x, s->x_dtype, s->rows, s->K, made, made_scale, stm),
@@ -149,6 +149,17 @@ moe_status moe_linear_w8a8(const moe_w8_shape* s, const void* x, const float* x_
     if (st) return st;
   }
   return launched(moe::launch_linear_w8a8(l, stm, false), "moe_linear_w8a8 launch");
+}
+
+moe_status moe_linear_w8a8_plan(const moe_w8_shape* s, int32_t* plan) {
+  const moe_status st = check_linear(s);
+  if (st) return st;
+  if (!plan) return fail(MOE_EINVAL, "plan is NULL");
+  const moe::LinearI8Plan p = moe::linear_w8a8_plan(s->rows, s->K, s->N, s->act);
+  plan[0] = p.kernel;
+  plan[1] = p.depth;
+  plan[2] = s->x_dtype == MOE_INT8 ? 0 : p.makes_codes ? 1 : 2;
+  return MOE_OK;
 }
 
 size_t moe_layer_w8a8_workspace(const moe_shape* s) {

@@ -22,12 +22,18 @@ struct LinearI8 {
   int y_type;
   int rows, K, N, act;
 };
+// The kernel of a product: mm_forward_plan's numbers, or kPlanRings (linear_few.h) with the
+// depth of its rings. makes_codes: of values, whose codes the product's launch makes.
+constexpr int kPlanRings = 8;
+struct LinearI8Plan {
+  int kernel, depth;
+  bool makes_codes;
+};
+LinearI8Plan linear_w8a8_plan(int rows, int K, int N, int act);
 // check: nothing is launched; hipErrorInvalidConfiguration where the launch would hold
 // 2^32 threads or more.
 hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check);
-// Few rows of values (x_type 0 or 1): their codes are made in the product's launch (q and
-// q_scale are not read).
-bool linear_w8a8_makes_codes(const LinearI8& l);
+// Values (x_type 0 or 1) of a plan that makes their codes (q and q_scale are not read).
 hipError_t launch_linear_w8a8_values(const LinearI8& l, const void* x, int x_type, hipStream_t s);
 
 // out[p] = (q[src(p)] . W_e^T) scaled, float32, for the rows p of each expert e; src(p) =

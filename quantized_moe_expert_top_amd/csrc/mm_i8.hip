@@ -69,9 +69,10 @@ hipError_t few_go(const LinearI8& l, const void* x, hipStream_t s) {
                      static_cast<size_t>(linear_lds(D, l.rows, l.K)), s, l, x);
   return hipGetLastError();
 }
+inline int ring_depth(int rows, int K) { return linear_lds(8, rows, K) <= kLinearLds ? 8 : 4; }
 template <bool VALUES, class XT, class O, bool OUT32>
 hipError_t few_depth(const LinearI8& l, const void* x, hipStream_t s) {
-  if (linear_lds(8, l.rows, l.K) <= kLinearLds) return few_go<VALUES, XT, O, OUT32, 8>(l, x, s);
+  if (ring_depth(l.rows, l.K) == 8) return few_go<VALUES, XT, O, OUT32, 8>(l, x, s);
   return few_go<VALUES, XT, O, OUT32, 4>(l, x, s);
 }
 template <bool VALUES, class XT>
@@ -80,23 +81,29 @@ hipError_t few_out(const LinearI8& l, const void* x, hipStream_t s) {
   return l.y_type == 1 ? few_depth<VALUES, XT, fp16_tag, false>(l, x, s)
                        : few_depth<VALUES, XT, bf16_tag, false>(l, x, s);
 }
-bool few_rows(const LinearI8& l) {
-  const long long tiles = l.act == kActSwiglu ? l.N / 16 : (l.N + 15) / 16;
-  return l.rows <= kFewTokens && tiles <= static_cast<long long>(kFewBlocks) * kLinearTiles &&
-         linear_lds(4, l.rows, l.K) <= kLinearLds;
-}
 
 }  // namespace
 
-bool linear_w8a8_makes_codes(const LinearI8& l) {
-  return few_rows(l) && static_cast<long long>(l.rows) * l.K <= kFewValues;
+LinearI8Plan linear_w8a8_plan(int rows, int K, int N, int act) {
+  const long long tiles = act == kActSwiglu ? N / 16 : (N + 15) / 16;
+  if (rows <= kFewTokens && tiles <= static_cast<long long>(kFewBlocks) * kLinearTiles &&
+      linear_lds(4, rows, K) <= kLinearLds)
+    return {kPlanRings, ring_depth(rows, K), static_cast<long long>(rows) * K <= kFewValues};
+  int plan = mm_forward_plan(rows, 0, N, K / 2, act);
+  // Two tiles of 32 rows over all CUs and more: their second round takes as long as the
+  // first, however few rows it has (33 x 4096 x 7168, SwiGLU: 22.8 us, tiles of 64 x 64
+  // 14.2; 32 rows, one tile: 13.1 against 13.3).
+  if (plan == 7 && rows > 32 && mm_row_tiles(32, rows, 0) * ((N + 15) / 16) > kFewBlocks)
+    plan = mm_pick_rows(rows, 0, N, K / 2, act).geom;
+  return {plan, 0, false};
 }
 hipError_t launch_linear_w8a8_values(const LinearI8& l, const void* x, int x_type, hipStream_t s) {
   return x_type == 1 ? few_out<true, fp16_tag>(l, x, s) : few_out<true, bf16_tag>(l, x, s);
 }
 
 hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
-  if (few_rows(l)) return check ? hipSuccess : few_out<false, bf16_tag>(l, nullptr, s);
+  const int plan = linear_w8a8_plan(l.rows, l.K, l.N, l.act).kernel;
+  if (plan == kPlanRings) return check ? hipSuccess : few_out<false, bf16_tag>(l, nullptr, s);
   MMArgs a = {};
   a.A = l.q;
   a.B = l.w;
@@ -112,12 +119,6 @@ hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
   a.kdim = l.K / 2;
   a.act = l.act;
   a.c_f32 = l.y_type == 2;
-  int plan = mm_forward_plan(l.rows, 0, l.N, l.K / 2, l.act);
-  // Two tiles of 32 rows over all CUs and more: their second round takes as long as the
-  // first, however few rows it has (33 x 4096 x 7168, SwiGLU: 22.8 us, tiles of 64 x 64
-  // 14.2; 32 rows, one tile: 13.1 against 13.3).
-  if (plan == 7 && l.rows > 32 && mm_row_tiles(32, l.rows, 0) * ((l.N + 15) / 16) > kFewBlocks)
-    plan = mm_pick_rows(l.rows, 0, l.N, l.K / 2, l.act).geom;
   return l.y_type == 1 ? launch<i8_tag<fp16_tag>>(a, plan, s, check)
                        : launch<i8_tag<bf16_tag>>(a, plan, s, check);
 }
