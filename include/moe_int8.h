@@ -122,6 +122,20 @@ MOE_API moe_status moe_layer_w8a8(const moe_shape* shape, const float* logits, c
                                   void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/*
+ * moe_layer_w8a8_plan — the kernels that a layer of this shape runs on, as
+ * moe_linear_w8a8_plan.
+ *   plan      int32 [5], written:
+ *     [0]  0 weights through rings of the waves, codes of all rows in LDS; 1 codes through
+ *          the rings too, in units of 16 rows of an expert; 2 grouped tiles; 3 the tiles
+ *          of moe_grouped_w8a8_ffn
+ *     [1]  gate/up: with 0 and 1 the depth of the rings, with 2 the tiles as
+ *          moe_product_plan's [0], else 0;  [2] the codes: 1 made in the product's launch,
+ *          2 in one before it
+ *     [3], [4]  the same for down
+ */
+MOE_API moe_status moe_layer_w8a8_plan(const moe_shape* shape, int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,8 +24,8 @@ from ._block import (  # noqa: F401
 )
 
 from ._int8 import (  # noqa: F401
-    layer_w8a8, layer_w8a8_workspace, linear_w8a8, linear_w8a8_plan, linear_w8a8_workspace,
-    quant_rows,
+    layer_w8a8, layer_w8a8_plan, layer_w8a8_workspace, linear_w8a8, linear_w8a8_plan,
+    linear_w8a8_workspace, quant_rows,
 )
 
 __all__ = ["MoeError", "LayerBuffers", "moe_forward", "moe_layer", "load", "router_logits",
@@ -35,7 +35,7 @@ __all__ = ["MoeError", "LayerBuffers", "moe_forward", "moe_layer", "load", "rout
            "grouped_mm", "grouped_mm_backward", "linear", "linear_backward", "block_norm",
            "block_norm_backward", "combine_backward", "product_plan", "layer_norm",
            "layer_norm_backward", "quant_rows", "linear_w8a8", "linear_w8a8_plan",
-           "layer_w8a8"]
+           "layer_w8a8", "layer_w8a8_plan"]
 
 
 @dataclass

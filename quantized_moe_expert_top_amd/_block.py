@@ -82,6 +82,7 @@ def _load() -> ctypes.CDLL:
             "moe_linear_w8a8": (INT, [w8] + [P] * 8 + [SZ, P]),
             "moe_linear_w8a8_plan": (INT, [w8, P]),
             "moe_layer_w8a8_workspace": (SZ, [layer]),
+            "moe_layer_w8a8_plan": (INT, [layer, P]),
             "moe_layer_w8a8": (INT, [layer, P, P, I32] + [P] * 9 + [I32, P, SZ, P]),
         }
         for name, (res, args) in sig.items():

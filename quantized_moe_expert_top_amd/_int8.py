@@ -11,7 +11,8 @@ from ._block import _act, _done, _ext, _load
 
 EXPORTS = ("moe_quant_rows", "moe_linear_w8a8_workspace", "moe_linear_w8a8",
            "moe_linear_w8a8_plan",
-           "moe_layer_w8a8_workspace", "moe_layer_w8a8")
+           "moe_layer_w8a8_workspace", "moe_layer_w8a8",
+           "moe_layer_w8a8_plan")
 
 
 def quant_rows(x, q, scale, stream=None) -> None:
@@ -80,3 +81,19 @@ def layer_w8a8(logits, x, w13, s13, w2, s2, topk_ids, topk_w, out, ws, residual=
     st = (_block._binding or _ext()).layer_w8a8(*args)
     if st:
         _done("moe_layer_w8a8", st, lambda: _block._binding.layer_w8a8(*args))
+
+
+_WAYS = ("rings", "rings by 16 rows", "tiles", "tiles of the grouped FFN")
+
+
+def layer_w8a8_plan(T: int, H: int, I: int, E: int, k: int) -> dict:
+    """The kernels that layer_w8a8 runs on for this shape, for tests and tuning: the way,
+    and for gate_up and down (the depth of their rings or their tiles' name, where the codes
+    are made)."""
+    s = _lib.MoeShape(T, H, I, E, k)
+    plan = (ctypes.c_int32 * 5)()
+    _lib._check("moe_layer_w8a8_plan", _load().moe_layer_w8a8_plan(ctypes.byref(s), plan))
+    way, up, up_codes, down, down_codes = plan
+    take = (lambda v: v, lambda v: v, lambda v: _block._TILES[v], lambda v: None)[way]
+    return dict(way=_WAYS[way], gate_up=(take(up), _CODES[up_codes]),
+                down=(take(down), _CODES[down_codes]))

@@ -217,4 +217,17 @@ moe_status moe_layer_w8a8(const moe_shape* s, const float* logits, const void* x
                   "moe_layer_w8a8 launch");
 }
 
+moe_status moe_layer_w8a8_plan(const moe_shape* s, int32_t* plan) {
+  const moe_status st = moe_api::check_shape(s, 16, 16);
+  if (st) return st;
+  if (!plan) return fail(MOE_EINVAL, "plan is NULL");
+  const moe::LayerI8Plan p = moe::layer_w8a8_plan(s->T, s->H, s->I, s->E, s->k);
+  plan[0] = p.way;
+  plan[1] = p.up.take;
+  plan[2] = p.up.makes_codes ? 1 : 2;
+  plan[3] = p.down.take;
+  plan[4] = p.down.makes_codes ? 1 : 2;
+  return MOE_OK;
+}
+
 }  // extern "C"

@@ -66,6 +66,17 @@ struct LayerI8 {
   int x_type, out_type;   // x: 0 or 1
   int T, H, I, E, k;
 };
+// The kernels of a layer: a way, and for each of its products what it takes there.
+enum LayerWay { kWayRings, kWayRingsByRows, kWayTiles, kWayLargeTiles };
+struct LayerI8Half {
+  int take;           // the depth of its rings; kWayTiles: mm_forward_plan's number
+  bool makes_codes;   // codes made in the product's launch
+};
+struct LayerI8Plan {
+  LayerWay way;
+  LayerI8Half up, down;
+};
+LayerI8Plan layer_w8a8_plan(int T, int H, int I, int E, int k);
 size_t layer_w8a8_workspace_bytes(int T, int H, int I, int E, int k);
 hipError_t launch_layer_w8a8(const LayerI8& l, void* ws, hipStream_t s);
 

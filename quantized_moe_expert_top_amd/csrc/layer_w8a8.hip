@@ -1,5 +1,6 @@
 // The whole routed layer on int8 weights in one call (moe_layer_w8a8).
 #include "launch.h"
+#include "launch_block.h"
 #include "layer_rows.h"
 #include "launch_int8.h"
 #include "mm_launch.h"
@@ -115,35 +116,33 @@ hipError_t few_go(const FewArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3(kFewBlocks), dim3(kFewThreads), few_lds<D>(KIND, a.T, a.H, a.I, a.k), s, a);
   return hipGetLastError();
 }
+int few_depth(int kind, int T, int H, int I, int k) {
+  return few_lds<8>(kind, T, H, I, k) <= size_t{kFewLds}   ? 8
+         : few_lds<4>(kind, T, H, I, k) <= size_t{kFewLds} ? 4
+         : few_lds<2>(kind, T, H, I, k) <= size_t{kFewLds} ? 2 : 0;
+}
 template <int KIND, bool CODES, class T, bool OUT32, int S>
-hipError_t few_depth(const FewArgs& a, hipStream_t s) {
-  if (few_lds<8>(KIND, a.T, a.H, a.I, a.k) <= size_t{kFewLds}) return few_go<KIND, CODES, T, OUT32, S, 8>(a, s);
-  if (few_lds<4>(KIND, a.T, a.H, a.I, a.k) <= size_t{kFewLds}) return few_go<KIND, CODES, T, OUT32, S, 4>(a, s);
+hipError_t few_at(const FewArgs& a, int depth, hipStream_t s) {
+  if (depth == 8) return few_go<KIND, CODES, T, OUT32, S, 8>(a, s);
+  if (depth == 4) return few_go<KIND, CODES, T, OUT32, S, 4>(a, s);
   return few_go<KIND, CODES, T, OUT32, S, 2>(a, s);
 }
 template <class T, int S>
-hipError_t few_gateup(const FewArgs& a, hipStream_t s) {
-  // In the block up to kFewValues values: 4096 (two tokens of 2048) 25.0 against 26.4 us
-  // for the layer with codes made ahead, 14336 118.8 against 119.9, 28672 117.4 against 115.5
-  if (a.T <= kFewWaves && a.T * a.H <= kFewValues) return few_depth<0, false, T, false, S>(a, s);
+hipError_t few_gateup(const FewArgs& a, const LayerI8Half& p, hipStream_t s) {
+  if (p.makes_codes) return few_at<0, false, T, false, S>(a, p.take, s);
   layer_route_kernel<T, S><<<a.T + (a.T + 3) / 4, 256, 0, s>>>(a, const_cast<int8_t*>(a.xq), const_cast<float*>(a.xs));
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : few_depth<0, true, bf16_tag, false, 1>(a, s);
+  return e != hipSuccess ? e : few_at<0, true, bf16_tag, false, 1>(a, p.take, s);
 }
 template <class T, bool OUT32>
-hipError_t few_down(const FewArgs& a, hipStream_t s) {
-  const int R = a.T * a.k;
-  // 12288 values of h 25.0 against 25.4 us, 18432 30.8 against 30.1
-  if (static_cast<long long>(R) * a.I <= kFewValues) return few_depth<1, false, T, OUT32, 1>(a, s);
-  const hipError_t e = launch_quant_rows(a.h, 2, R, a.I, const_cast<int8_t*>(a.hq), const_cast<float*>(a.hs), s);
-  return e != hipSuccess ? e : few_depth<1, true, T, OUT32, 1>(a, s);
+hipError_t few_down(const FewArgs& a, const LayerI8Half& p, hipStream_t s) {
+  if (p.makes_codes) return few_at<1, false, T, OUT32, 1>(a, p.take, s);
+  const hipError_t e = launch_quant_rows(a.h, 2, a.T * a.k, a.I, const_cast<int8_t*>(a.hq), const_cast<float*>(a.hs), s);
+  return e != hipSuccess ? e : few_at<1, true, T, OUT32, 1>(a, p.take, s);
 }
 template <class T>
-hipError_t few_up(const FewArgs& a, hipStream_t s) {
-  return a.E <= 128 ? few_gateup<T, 2>(a, s) : a.E <= 256 ? few_gateup<T, 4>(a, s) : few_gateup<T, 16>(a, s);
-}
-bool few_fits(int T, int H, int I, int k) {
-  return T <= kFewTokens && few_lds<2>(0, T, H, I, k) <= size_t{kFewLds} && few_lds<2>(1, T, H, I, k) <= size_t{kFewLds};
+hipError_t few_up(const FewArgs& a, const LayerI8Half& p, hipStream_t s) {
+  return a.E <= 128 ? few_gateup<T, 2>(a, p, s) : a.E <= 256 ? few_gateup<T, 4>(a, p, s) : few_gateup<T, 16>(a, p, s);
 }
 
 // Up to 512 picks: those whose codes do not fit in LDS, and more than 16 tokens while
@@ -176,6 +175,24 @@ hipError_t route(const FewArgs& a, Ws& w, hipStream_t s) {
 
 }  // namespace
 
+LayerI8Plan layer_w8a8_plan(int T, int H, int I, int E, int k) {
+  const int R = T * k;
+  const int up = few_depth(0, T, H, I, k), down = few_depth(1, T, H, I, k);
+  // Codes are made in a product's own launch up to kFewValues values. Of x: 4096 (two tokens
+  // of 2048) 25.0 against 26.4 us for the layer with codes made ahead, 14336 118.8 against
+  // 119.9, 28672 117.4 against 115.5. Of h: 12288 25.0 against 25.4, 18432 30.8 against 30.1.
+  if (T > 0 && T <= kFewTokens && up && down)
+    return {kWayRings, {up, T <= kFewWaves && T * H <= kFewValues},
+            {down, static_cast<long long>(R) * I <= kFewValues}};
+  if (T > 0 && rows_fit(T, E, k)) return {kWayRingsByRows, {kRowsDepth, false}, {kRowsDepth, false}};
+  // Products of few rows an expert stream weights, which the low tiles do better; from 96
+  // rows on the 128-row tiles of the grouped FFN do (2048 x 768, 128 experts, the layer:
+  // 512 tokens 167 against 173 us, 4096 tokens 427 against 387).
+  if (R > 96LL * (R < E ? R : E)) return {kWayLargeTiles, {0, false}, {0, false}};
+  return {kWayTiles, {mm_forward_plan(R, E, 2 * I, H / 2, kActSwiglu), false},
+          {mm_forward_plan(R, E, H, I / 2, 0), false}};
+}
+
 size_t layer_w8a8_workspace_bytes(int T, int H, int I, int E, int k) {
   return carve(nullptr, T, H, I, E, k).total;
 }
@@ -186,14 +203,16 @@ hipError_t launch_layer_w8a8(const LayerI8& l, void* base, hipStream_t s) {
   if (l.offsets) w.offsets = l.offsets;
   const FewArgs few = {l.logits, l.x, w.xq, w.xs, w.hq, w.hs, l.w13, l.s13, l.w2, l.s2, l.residual, l.ids, l.w,
                        l.offsets, w.record, w.h, l.out, T, H, I, E, k};
-  if (T > 0 && few_fits(T, H, I, k)) {
-    const hipError_t e = l.x_type == 1 ? few_up<fp16_tag>(few, s) : few_up<bf16_tag>(few, s);
+  const LayerI8Plan plan = layer_w8a8_plan(T, H, I, E, k);
+  const int R = T * k;
+  if (plan.way == kWayRings) {
+    const hipError_t e = l.x_type == 1 ? few_up<fp16_tag>(few, plan.up, s) : few_up<bf16_tag>(few, plan.up, s);
     if (e != hipSuccess) return e;
-    return l.out_type == 2 ? few_down<bf16_tag, true>(few, s)
-         : l.out_type == 1 ? few_down<fp16_tag, false>(few, s) : few_down<bf16_tag, false>(few, s);
+    return l.out_type == 2 ? few_down<bf16_tag, true>(few, plan.down, s)
+         : l.out_type == 1 ? few_down<fp16_tag, false>(few, plan.down, s)
+                           : few_down<bf16_tag, false>(few, plan.down, s);
   }
-  if (T > 0 && rows_fit(T, E, k)) {
-    const int R = T * k;
+  if (plan.way == kWayRingsByRows) {
     hipError_t e = l.x_type == 1 ? route<fp16_tag>(few, w, s) : route<bf16_tag>(few, w, s);
     if (e != hipSuccess) return e;
     e = rows_go<0>({w.xq, w.xs, l.w13, l.s13, l.ids, w.h, l.offsets, w.rows_record, T, R, H, I, E, k}, s);
@@ -210,11 +229,7 @@ hipError_t launch_layer_w8a8(const LayerI8& l, void* base, hipStream_t s) {
   if (e != hipSuccess || T == 0) return e;
   e = launch_quant_rows(l.x, l.x_type, T, H, w.xq, w.xs, s);
   if (e != hipSuccess) return e;
-  // Products of few rows an expert stream weights, which the low tiles do better; from 96
-  // rows on the 128-row tiles of the grouped FFN do (2048 x 768, 128 experts, the layer:
-  // 512 tokens 167 against 173 us, 4096 tokens 427 against 387).
-  const int R = T * k;
-  const bool low = R <= 96LL * (R < E ? R : E);
+  const bool low = plan.way == kWayTiles;
   e = low ? launch_grouped_i8({w.xq, w.xs, l.w13, l.s13, w.offsets, w.sorted, w.h, R, T, k, E, H, 2 * I, true}, s)
           : launch_w8a8_gateup(T, H, I, E, k, w.xq, w.xs, l.w13, l.s13, w.offsets, w.sorted, w.h, nullptr, s);
   if (e != hipSuccess) return e;
