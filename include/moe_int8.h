@@ -14,11 +14,11 @@
  * streams with distinct workspaces may run concurrently; two runs on the same inputs
  * give identical bits. A workspace holds nothing between calls.
  *
- * Codes of a row (the rule of moe_grouped_w8a8_ffn): s = max|x| / 127 in float32 (IEEE
- * division), q = x / s to the nearest whole number, ties to even, clamped to
- * [-127, 127]; s = 0 and q = 0 for a row of zeros. A row that holds an infinity or a
- * NaN gets s = NaN and q = 0: all that is computed from it is NaN, and other rows are
- * not touched.
+ * Codes of a row: s = max|x| / 127 in float32 (IEEE division), q = x / s to the nearest
+ * whole number, ties to even, clamped to [-127, 127]; s = 0 and q = 0 for a row of zeros.
+ * For rows of finite values that is the rule of moe_grouped_w8a8_ffn, which has none for
+ * others; here a row that holds an infinity or a NaN gets s = NaN and q = 0: all that is
+ * computed from it is NaN, and other rows are not touched.
  */
 #ifndef MOE_INT8_H
 #define MOE_INT8_H
@@ -110,9 +110,13 @@ MOE_API moe_status moe_linear_w8a8_plan(const moe_w8_shape* shape, int32_t* plan
  *             moe_expert_counts_accumulate)
  *   out       out_dtype (MOE_BF16, MOE_FP16 or MOE_F32) [T, H]
  * Requires what moe_grouped_w8a8_ffn does. `ws` must hold
- * moe_layer_w8a8_workspace(shape) bytes. A few tokens take two launches, some tens five;
- * a result is the definition's rounded as above whichever ran, but its last bit may differ
- * between them (a value of h next to the border of two codes may take either).
+ * moe_layer_w8a8_workspace(shape) bytes. Few tokens (up to 16 whose codes fit in LDS) take
+ * two to four launches: two where T <= 8, T*H <= 16384 and T*k*I <= 16384; some tens take
+ * five, more tokens seven to nine.
+ * Which kernels run depends on the shape alone, and each result is the definition's, h
+ * within its float32 roundings. Between kernels a code of h whose quotient lies next to
+ * the middle of two whole numbers may be either of them: each such code moves the outputs
+ * of its token by topk_w * s * w2 * s2, with s the scale of its row of h.
  */
 MOE_API size_t moe_layer_w8a8_workspace(const moe_shape* shape);
 MOE_API moe_status moe_layer_w8a8(const moe_shape* shape, const float* logits, const void* x,

@@ -5,7 +5,7 @@
 // rows, 16 at a time, through a ring of its own in LDS, 128 bytes of k of every row a step,
 // D steps ahead: a wave load takes 8 rows x 128 bytes, whole cache lines, and nothing waits
 // for other waves. (Loads straight into operand registers, 16 rows x 64 bytes each, streamed
-// 235 MB at 4.0 TB/s where this reaches 5.5.) v_mfma_i32_16x16x64 multiplies the 16 weight
+// 235 MB at 4.0 TB/s where this reaches 5.9.) v_mfma_i32_16x16x64 multiplies the 16 weight
 // rows with up to 16 rows of codes; int32 sums are exact.
 #pragma once
 #include "quant.h"

@@ -1,8 +1,10 @@
 // The W8A8 layer for a few tokens (moe_layer_w8a8), bound by the bytes of the picked
-// experts' weights: two kernels, gate/up and down with the combine. One token of 7168 x
-// 2048, 8 experts: gate/up 40 us, 235 MB at 5.9 TB/s, down 24 us, 117 MB at 4.9; two tokens
-// of 2048 x 768: 13.2 us for 47 MB and 9.8 for 24, which by themselves stream in 8 and 4; the
-// rest is the launch, the picks, the codes and the rings' first loads, one after another.
+// experts' weights: two kernels, gate/up and down with the combine, and before each a small
+// one where its codes are more than its blocks make in time (layer_w8a8_plan). One token of
+// 7168 x 2048, 8 experts: gate/up 40 us, 235 MB at 5.9 TB/s, down 24 us, 117 MB at 4.9; two
+// tokens of 2048 x 768: 13.2 us for 47 MB and 9.8 for 24, which by themselves stream in 8 and
+// 4; the rest is the launch, the picks, the codes and the rings' first loads, one after
+// another.
 #pragma once
 #include "../../include/moe.h"
 #include "few.h"

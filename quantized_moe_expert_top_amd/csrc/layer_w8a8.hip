@@ -116,6 +116,8 @@ hipError_t few_go(const FewArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3(kFewBlocks), dim3(kFewThreads), few_lds<D>(KIND, a.T, a.H, a.I, a.k), s, a);
   return hipGetLastError();
 }
+// Gate/up that makes its codes has 8 always: the lower depths are compiled for it and not
+// taken.
 int few_depth(int kind, int T, int H, int I, int k) {
   return few_lds<8>(kind, T, H, I, k) <= size_t{kFewLds}   ? 8
          : few_lds<4>(kind, T, H, I, k) <= size_t{kFewLds} ? 4
@@ -185,9 +187,11 @@ LayerI8Plan layer_w8a8_plan(int T, int H, int I, int E, int k) {
     return {kWayRings, {up, T <= kFewWaves && T * H <= kFewValues},
             {down, static_cast<long long>(R) * I <= kFewValues}};
   if (T > 0 && rows_fit(T, E, k)) return {kWayRingsByRows, {kRowsDepth, false}, {kRowsDepth, false}};
-  // Products of few rows an expert stream weights, which the low tiles do better; from 96
-  // rows on the 128-row tiles of the grouped FFN do (2048 x 768, 128 experts, the layer:
-  // 512 tokens 167 against 173 us, 4096 tokens 427 against 387).
+  // Products of few rows an expert stream weights, which the low tiles do better; of more
+  // rows the 128-row tiles of the grouped FFN do. The layer by low and by 128-row tiles, us,
+  // 2048 x 768, 8 of 128 experts: 32 rows an expert 166 and 173, 64 208 and 203, 96 261 and
+  // 235, 128 280 and 256, 256 427 and 387; 4096 x 1536, 4 of 16 experts: 16 rows 92 and 96,
+  // 64 114 and 120, 96 128 and 126, 128 160 and 154.
   if (R > 96LL * (R < E ? R : E)) return {kWayLargeTiles, {0, false}, {0, false}};
   return {kWayTiles, {mm_forward_plan(R, E, 2 * I, H / 2, kActSwiglu), false},
           {mm_forward_plan(R, E, H, I / 2, 0), false}};

@@ -2,8 +2,9 @@
 // z = (sum_k q_tk w_nk) s_t u_n + b_n, on the tile and few-row kernels of the 16-bit
 // products (mm.h, mm_few.h). Bytes and matrix time of K codes are those of K / 2
 // 16-bit values, so the choice of a kernel is theirs for that K. 8192 x 7168 -> SwiGLU
-// 4096: 206 us, 2.33 POP/s, bound by the matrix pipes and the clock under their load (a
-// plain library product of these sizes reaches 2.18, 16384^2 x 8192 2.41).
+// 4096: 206 us, 2.33 POP/s; the matrix pipes are busy 61% of that at 1.78 GHz and the waves
+// wait for 29% of their life, so the waits bound it, not the pipes' rate (a plain library
+// product of these sizes reaches 2.18, 16384^2 x 8192 2.41, register operands alone 4.2).
 #include "launch_block.h"
 #include "launch_int8.h"
 #include "linear_few.h"
@@ -69,6 +70,8 @@ hipError_t few_go(const LinearI8& l, const void* x, hipStream_t s) {
                      static_cast<size_t>(linear_lds(D, l.rows, l.K)), s, l, x);
   return hipGetLastError();
 }
+// Rows of values whose codes the block makes leave room for 8: the lower depth is compiled
+// for them and not taken.
 inline int ring_depth(int rows, int K) { return linear_lds(8, rows, K) <= kLinearLds ? 8 : 4; }
 template <bool VALUES, class XT, class O, bool OUT32>
 hipError_t few_depth(const LinearI8& l, const void* x, hipStream_t s) {
@@ -86,6 +89,9 @@ hipError_t few_out(const LinearI8& l, const void* x, hipStream_t s) {
 
 LinearI8Plan linear_w8a8_plan(int rows, int K, int N, int act) {
   const long long tiles = act == kActSwiglu ? N / 16 : (N + 15) / 16;
+  // The codes of values are made in the product's launch as far as its registers hold the
+  // values (kFewValues): 1 x 2048 -> 2048 4.8 us against 7.1 with a launch before it, 2 x
+  // 7168 -> SwiGLU 4096 9.0 against 10.8, 16 x 1024 -> 2048 6.9 against 7.1.
   if (rows <= kFewTokens && tiles <= static_cast<long long>(kFewBlocks) * kLinearTiles &&
       linear_lds(4, rows, K) <= kLinearLds)
     return {kPlanRings, ring_depth(rows, K), static_cast<long long>(rows) * K <= kFewValues};
