@@ -138,17 +138,18 @@ moe_status moe_linear_w8a8(const moe_w8_shape* s, const void* x, const float* x_
   l.N = s->N;
   l.act = s->act;
   const hipStream_t stm = static_cast<hipStream_t>(stream);
-  if (moe::launch_linear_w8a8(l, stm, true) != hipSuccess)
+  const moe::LinearI8Plan plan = moe::linear_w8a8_plan(s->rows, s->K, s->N, s->act);
+  if (moe::launch_linear_w8a8(l, plan, stm, true) != hipSuccess)
     return fail(MOE_ESHAPE, "a launch of these sizes would hold 2^32 threads or more");
   if ((st = check_device()) != MOE_OK) return st;
-  if (!codes && moe::linear_w8a8_plan(s->rows, s->K, s->N, s->act).makes_codes)
+  if (!codes && plan.makes_codes)
     return launched(moe::launch_linear_w8a8_values(l, x, s->x_dtype, stm), "moe_linear_w8a8 launch");
   if (!codes) {
     st = launched(moe::launch_quant_rows(x, s->x_dtype, s->rows, s->K, made, made_scale, stm),
                   "moe_linear_w8a8 codes launch");
     if (st) return st;
   }
-  return launched(moe::launch_linear_w8a8(l, stm, false), "moe_linear_w8a8 launch");
+  return launched(moe::launch_linear_w8a8(l, plan, stm, false), "moe_linear_w8a8 launch");
 }
 
 moe_status moe_linear_w8a8_plan(const moe_w8_shape* s, int32_t* plan) {

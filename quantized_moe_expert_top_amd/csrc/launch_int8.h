@@ -32,7 +32,7 @@ struct LinearI8Plan {
 LinearI8Plan linear_w8a8_plan(int rows, int K, int N, int act);
 // check: nothing is launched; hipErrorInvalidConfiguration where the launch would hold
 // 2^32 threads or more.
-hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check);
+hipError_t launch_linear_w8a8(const LinearI8& l, const LinearI8Plan& plan, hipStream_t s, bool check);
 // Values (x_type 0 or 1) of a plan that makes their codes (q and q_scale are not read).
 hipError_t launch_linear_w8a8_values(const LinearI8& l, const void* x, int x_type, hipStream_t s);
 

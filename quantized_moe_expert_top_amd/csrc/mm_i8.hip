@@ -107,9 +107,8 @@ hipError_t launch_linear_w8a8_values(const LinearI8& l, const void* x, int x_typ
   return x_type == 1 ? few_out<true, fp16_tag>(l, x, s) : few_out<true, bf16_tag>(l, x, s);
 }
 
-hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
-  const int plan = linear_w8a8_plan(l.rows, l.K, l.N, l.act).kernel;
-  if (plan == kPlanRings) return check ? hipSuccess : few_out<false, bf16_tag>(l, nullptr, s);
+hipError_t launch_linear_w8a8(const LinearI8& l, const LinearI8Plan& plan, hipStream_t s, bool check) {
+  if (plan.kernel == kPlanRings) return check ? hipSuccess : few_out<false, bf16_tag>(l, nullptr, s);
   MMArgs a = {};
   a.A = l.q;
   a.B = l.w;
@@ -125,8 +124,8 @@ hipError_t launch_linear_w8a8(const LinearI8& l, hipStream_t s, bool check) {
   a.kdim = l.K / 2;
   a.act = l.act;
   a.c_f32 = l.y_type == 2;
-  return l.y_type == 1 ? launch<i8_tag<fp16_tag>>(a, plan, s, check)
-                       : launch<i8_tag<bf16_tag>>(a, plan, s, check);
+  return l.y_type == 1 ? launch<i8_tag<fp16_tag>>(a, plan.kernel, s, check)
+                       : launch<i8_tag<bf16_tag>>(a, plan.kernel, s, check);
 }
 
 }  // namespace moe
