@@ -6,6 +6,7 @@ PyTorch only provides device memory and the stream.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 from . import _lib
@@ -118,9 +119,14 @@ def moe_layer(b: LayerBuffers, x, logits, weights, stream=None):
     if b.fmt == "w8a8":
         import torch
         x = x.view(torch.bfloat16) if x.dtype == torch.int16 else x   # bf16 bits
-        need = layer_w8a8_workspace(b.T, b.H, b.I, b.E, b.k)
-        if b.layer_ws.numel() < need:
-            b.layer_ws = torch.empty(need, dtype=torch.uint8, device=b.out.device)
+        if b.layer_ws.numel() <= 16:   # alloc's
+            # from the memory of the stream that uses it: what another stream has freed may
+            # still be in use there
+            on = (contextlib.nullcontext() if stream is None or not b.out.is_cuda else
+                  torch.cuda.stream(torch.cuda.ExternalStream(stream, device=b.out.device)))
+            with on:
+                b.layer_ws = torch.empty(layer_w8a8_workspace(b.T, b.H, b.I, b.E, b.k),
+                                         dtype=torch.uint8, device=b.out.device)
         layer_w8a8(logits, x, w13, s13, w2, s2, b.ids, b.w, b.out, b.layer_ws,
                    expert_offsets=b.offsets, stream=stream)
         return b.out

@@ -60,3 +60,28 @@ def test_first_call_in_a_capture(T):
         moe.moe_layer(b, x, logits, (w13, s13, w2, s2))
         torch.cuda.synchronize()
         assert torch.equal(b.out, want)
+
+
+@pytest.mark.gpu
+def test_first_call_on_a_named_stream():
+    """The workspace comes from that stream's memory, not from what the current stream freed
+    last and may still be using."""
+    T, H, I, E, k = 5, 256, 128, 16, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    i8 = dict(generator=g, device="cuda", dtype=torch.int8)
+    weights = (torch.randint(-128, 128, (E, 2 * I, H), **i8), torch.rand((E, 2 * I), device="cuda") * 1e-3,
+               torch.randint(-128, 128, (E, H, I), **i8), torch.rand((E, H), device="cuda") * 1e-3)
+    x = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    want = moe.moe_layer(moe.LayerBuffers.alloc(T, H, I, E, k, "w8a8"), x, logits, weights).clone()
+    b, side = moe.LayerBuffers.alloc(T, H, I, E, k, "w8a8"), torch.cuda.Stream()
+    freed = torch.empty(moe.layer_w8a8_workspace(T, H, I, E, k), dtype=torch.uint8, device="cuda")
+    at = freed.data_ptr()
+    torch.cuda.synchronize()
+    del freed
+    out = moe.moe_layer(b, x, logits, weights, stream=side.cuda_stream)
+    side.synchronize()
+    assert b.layer_ws.data_ptr() != at
+    assert torch.equal(out, want)
+    b = moe.LayerBuffers.alloc(T, H, I, E, k, "w8a8")
+    assert torch.equal(moe.moe_layer(b, x, logits, weights, stream=0), want)   # the default stream by number
